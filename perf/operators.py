@@ -15,8 +15,6 @@ BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 DTYPES = {"bf16": BF16, "f32": F32, "e4m3": E4M3}
 E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0)
 INT4 = (0.0, 1.0, 2.0, 3.0, 4.0, 5.0, 6.0, 7.0, -8.0, -7.0, -6.0, -5.0, -4.0, -3.0, -2.0, -1.0)
-# Nibble p of a 32-bit word of eight codes belongs to channel NIBBLE[p]: even channels in the low half, odd ones in the high.
-NIBBLE = (0, 2, 4, 6, 1, 3, 5, 7)
 
 
 # ------------------------------------------------------------------------------------------------------------- cases
@@ -108,9 +106,8 @@ def _encode_e2m1(v):
 
 
 def _pack(codes):
-    """[..., n] codes in channel order -> [..., n / 2] bytes of 32-bit words of eight codes."""
-    q = codes.unflatten(-1, (-1, 8))[..., list(NIBBLE)].unflatten(-1, (4, 2))
-    return (q[..., 0] | (q[..., 1] << 4)).flatten(-2)
+    """[..., n] codes -> [..., n / 2] bytes, the even channel in the low half."""
+    return codes[..., 0::2] | (codes[..., 1::2] << 4)
 
 
 def _record_bytes(c, rd):
@@ -209,9 +206,8 @@ def prepare(case, seed):
 
 # ------------------------------------------------------------------------------------------------------- plain forms
 def _codes(b):
-    """Bytes of 32-bit words of eight codes -> the codes in channel order (as indices)."""
-    q = torch.stack((b & 15, b >> 4), -1).unflatten(-2, (-1, 4)).flatten(-2)
-    return q[..., [NIBBLE.index(i) for i in range(8)]].flatten(-2).int()
+    """Bytes [..., n / 2] -> their codes [..., n], as indices."""
+    return torch.stack((b & 15, b >> 4), -1).flatten(-2).int()
 
 
 def _values(rec, c, rd):
@@ -361,9 +357,9 @@ def _e2m1_of(code):
 
 
 def _row_codes(words):
-    """int32 words -> codes in channel order, by shifts: channel 2i at bit 4i, channel 2i + 1 at bit 16 + 4i."""
+    """int32 words (little-endian) -> codes in channel order, by shifts: channel j of eight at bit 4j."""
     w = words.long() & 0xFFFFFFFF
-    return torch.stack([(w >> (4 * (j // 2) + 16 * (j % 2))) & 15 for j in range(8)], -1).flatten(-2)
+    return torch.stack([(w >> (4 * j)) & 15 for j in range(8)], -1).flatten(-2)
 
 
 def _exact_rows(rec, c, rd):
