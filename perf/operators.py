@@ -295,7 +295,8 @@ def _own(s):
             s["desc"] = hb.w4_desc(s["T"], s["N"], s["K"], groups=s["groups"], scale_group=s["G"],
                                    code=hb.HCA_W4_E2M1 if s["code"] == "e2m1" else hb.HCA_W4_INT4,
                                    x_dtype=hb.DTYPE_CODE[s["x_"].dtype], out_dtype=hb.DTYPE_CODE[s["out_"].dtype])
-        hb.w4_linear(s["desc"], s["x_"], s["x_scale"], s["codes"], s["scales"], s["row_scale"], s["out_"])
+            s["ws"] = torch.empty(max(16, hb.w4_linear_workspace_size(s["desc"])), dtype=torch.uint8, device="cuda")
+        hb.w4_linear(s["desc"], s["x_"], s["x_scale"], s["codes"], s["scales"], s["row_scale"], s["out_"], s["ws"])
         return s["out_"]
     if s["op"] == "kv":
         hb.kv_quant_fp4(s["x_"], s["c"], s["rd"], s["cache"], slots=s["slots"])
