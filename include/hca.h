@@ -445,6 +445,137 @@ int hca_kv_dequant_mixed(const void *in, long long rows, int c, int rd, void *ou
  * ---------------------------------------------------------------------- */
 int hca_fp4_rotate_quant(const void *x, hca_dtype x_dtype, long long rows, int n, void *out, hca_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The low-bit decode step: what runs between two attention layers, and their
+ * attention, with 8-bit activations, 4-bit weights and a 4-bit KV cache.  The
+ * papers describe none of these calls; E2M1 values and power-of-two block
+ * scales are [J] §4.4's, sink, window, visibility and inverse RoPE those of
+ * csa_attend / hca_attend.
+ *
+ * 4-bit codes are packed two to a byte: channel 2j in the low half of byte j,
+ * channel 2j + 1 in the high half.  E2M1 code = sign << 3 | magnitude index
+ * into {0, .5, 1, 1.5, 2, 3, 4, 6}; INT4 code = two's complement, -8 .. 7.
+ * ---------------------------------------------------------------------- */
+
+/* Residual addition and RMSNorm of rows, optionally with an e4m3 output:
+ *   z = x + res (fp32),  res_out = z in res_dtype,
+ *   y = z * gamma / sqrt(mean(z^2) + eps),  out = y in out_dtype.
+ * out_dtype HCA_FP8E4M3: out holds codes and out_scale fp32 scales, y ~ code *
+ *   scale: scale = amax / 448 and code = nearest e4m3 (ties to even,
+ *   saturating) of y / scale, both divisions in fp32; an all-zero group has
+ *   scale 0 and codes 0.  scale_group 0: one scale per row, out_scale [rows];
+ *   64 or 128: one per that many channels, out_scale [rows, d / scale_group]
+ *   (d a multiple of it).  The norm is taken of the unrounded sum z.
+ * x, res, res_out, out: [rows, d], innermost contiguous, row r at r * ldx /
+ *   ldr / ldr / ldo elements (0 = dense; otherwise >= d).  res NULL: z = x.
+ *   res_out NULL: not written.  gamma [d] fp32, NULL = ones.
+ * res_out may be res itself (the same pointer); otherwise the bytes from an
+ *   output's first row to its last may not meet those of an input or of another
+ *   output.
+ * dtypes: x HCA_F32 or HCA_BF16; res_dtype x_dtype or HCA_F32; out HCA_F32,
+ *   HCA_BF16 or HCA_FP8E4M3.  1 <= d <= 32768; rows = 0 is a no-op.
+ * A row with an infinity or a NaN has an undefined e4m3 output; without one it
+ * follows the formula in fp32. */
+typedef struct {
+  long long rows;
+  int d;
+  hca_dtype x_dtype, res_dtype, out_dtype;
+  int scale_group;
+  float eps;                 /* <= 0 selects 1e-6 */
+  long long ldx, ldr, ldo;
+} hca_norm_desc;
+int hca_add_rms_norm(const hca_norm_desc *d, const void *x, const void *res, const float *gamma, void *res_out,
+                     void *out, float *out_scale, hca_stream_t stream);
+
+/* Products of a few tokens with 4-bit weights, `groups` of them side by side
+ * (groups = 1: one plain product; the grouped output projection's first stage
+ * has one per head group):
+ *   out[t, g*N + n] = x_scale[t] * row_scale[g*N + n] *
+ *       sum_k x[t, g*K + k] * scale[g, k / scale_group, n] * code[g*N + n, k]
+ * codes [groups*N, K/2] bytes; scales [groups, K/scale_group, ldn] e4m3 bytes
+ *   with ldn = N rounded up to 16; row_scale [groups*N] fp32.
+ * x [T, groups*K] HCA_BF16 (x_scale NULL) or HCA_FP8E4M3 (x_scale [T] fp32);
+ *   out [T, groups*N] HCA_F32 or HCA_BF16; row strides ldx, ldo elements
+ *   (0 = dense).  Sums are fp32 and run in a fixed order.
+ * K a multiple of 32 and of scale_group (32, 64 or 128), K <= 32768; N >= 1,
+ *   T >= 0 (T = 0 is a no-op), groups >= 1.  Rows of x must start at multiples
+ *   of 16 bytes.  Meant for decode batches: beyond 64 tokens the weights are
+ *   read once per 64.  x must be finite.
+ * ws: scratch of hca_w4_linear_workspace_size bytes (16-byte aligned), which
+ *   calls that may overlap in time must not share.  out may not overlap an
+ *   input or ws. */
+typedef enum { HCA_W4_E2M1 = 0, HCA_W4_INT4 = 1 } hca_w4_code;
+typedef struct {
+  int T, N, K, groups, scale_group;
+  hca_w4_code code;
+  hca_dtype x_dtype, out_dtype;
+  long long ldx, ldo;
+} hca_w4_desc;
+size_t hca_w4_linear_workspace_size(const hca_w4_desc *d);
+int hca_w4_linear(const hca_w4_desc *d, const void *x, const float *x_scale, const void *codes, const void *scales,
+                  const float *row_scale, void *out, void *ws, size_t ws_bytes, hca_stream_t stream);
+/* The weights of hca_w4_linear from w [groups*N, K] HCA_F32 or HCA_BF16 (T, the
+ * x / out fields and strides of d are not used).  Per row row_scale = amax /
+ * (top * 448), top = 6 (E2M1) or 7 (INT4); per group scale = nearest e4m3 of
+ * amax_group / top / row_scale; code = nearest (ties to even; saturating at
+ * +-top) of w / (row_scale * scale): each operation rounded to fp32, 0 where
+ * the divisor is 0.  Zero is stored as code 0.  Also clears the scales' padding
+ * columns.  Weights must be finite. */
+int hca_w4_quantize(const hca_w4_desc *d, const void *w, hca_dtype w_dtype, void *codes, void *scales,
+                    float *row_scale, hca_stream_t stream);
+
+/* 4-bit KV rows.  Record of one row, hca_kv_fp4_row_bytes(c, rd) bytes (a
+ * multiple of 16; 368 at c = 512, rd = 64, where bf16 takes 1024):
+ *   bytes [0, q/2)                 E2M1 codes of channels 0 .. q-1, q = c - rd
+ *   bytes [q/2, q/2+2rd)           channels q .. c-1 (the RoPE dims) as bf16
+ *   bytes [q/2+2rd, q/2+2rd+q/32)  one byte e + 127 per 32 code channels
+ *   then zero bytes up to the record size.
+ * e is the smallest exponent with amax <= 6 * 2^e, at least -126 (byte 0 for
+ * an all-zero block); code = nearest E2M1 (ties to the even code) of x / 2^e;
+ * zero is stored as +0.  A code channel's value is code * 2^e, exactly a bf16
+ * value.  Shapes as for the mixed-precision records.  Inputs must be finite.
+ * Rows and records: row r is record slots[r] of `records` (slots NULL: record
+ * r).  quant skips a row whose slot lies outside [0, records), so a slot of -1
+ * drops the row; the other slots of one call must be distinct (of two rows with
+ * one slot the record holds a mixture).  dequant writes a zero row for a slot
+ * outside [0, records).  rows = 0 is a no-op. */
+size_t hca_kv_fp4_row_bytes(int c, int rd);   /* 0 when (c, rd) is unsupported */
+int hca_kv_quant_fp4(const void *x, hca_dtype x_dtype, long long rows, int c, int rd, void *out, long long records,
+                     const long long *slots, hca_stream_t stream);
+int hca_kv_dequant_fp4(const void *in, long long records, const long long *slots, long long rows, int c, int rd,
+                       void *out, hca_stream_t stream);
+
+/* A cache of 4-bit records: contiguous, rows [B, cap] records (pages NULL), or
+ * paged: rows [n_pages, cap] records, entry e of sequence b in page
+ * pages[b, e / cap], record e % cap.  A page number outside [0, n_pages) makes
+ * its entries absent. */
+typedef struct {
+  const void *rows;
+  int cap;               /* records per sequence, or per page */
+  const int32_t *pages;  /* [B, max_pages] or NULL */
+  int max_pages, n_pages;
+} hca_fp4_cache;
+
+/* Decode attention (one query token per sequence, one position each) over a
+ * cache of 4-bit records: csa_attend / hca_attend's formula with
+ *   keys = window rows of tokens max(0, pos-w+1) .. pos from the ring kv_win
+ *   [B, w, c] (dtype rows, token p in slot p % w; w = 0: none) followed by the
+ *   entries idx[b, j], 0 <= j < d->k (idx != NULL), or every visible entry
+ *   0 .. (pos+1)/m - 1 (idx NULL).
+ * pos = positions[b] (device int32), clamped to max_pos; a negative position
+ * has no keys, and a sequence without keys gives zeros.  Entries that are not
+ * visible, lie beyond the cache's capacity or in an absent page, and idx < 0
+ * are skipped; an entry listed twice in idx counts twice.
+ * q, o [B, n_h, c] HCA_BF16, n_h <= 64, c in {128, 256, 512}, (c, rd) as in
+ * hca_kv_fp4_row_bytes; sink [n_h] fp32, NULL = no sink; kv_mixed must be 0;
+ * max_ctas as in hca_attend.  q and KV values must be finite.
+ * ws: scratch of hca_attend_fp4_workspace_size bytes (16-byte aligned), which
+ * calls that may overlap in time must not share. */
+size_t hca_attend_fp4_workspace_size(const hca_attn_desc *d, int max_pos);
+int hca_attend_fp4(const hca_attn_desc *d, const void *q, const hca_fp4_cache *cache, const int32_t *idx,
+                   const void *kv_win, const float *sink, const int32_t *positions, int max_pos, void *o, void *ws,
+                   size_t ws_bytes, hca_stream_t stream);
+
 /* Diagnostic timeline of the decode step's kernels (ingest, indexer, top-k,
  * attention): with buf set, thread 0 of every CTA of those kernels appends
  * one record of four uint64 -- entry time, time after its wait for the

@@ -19,6 +19,7 @@ HCA_OK, HCA_ERR_INVALID, HCA_ERR_UNSUPPORTED, HCA_ERR_CUDA, HCA_ERR_TIMEOUT = 0,
 HCA_F32, HCA_BF16, HCA_FP8E4M3, HCA_FP4 = 0, 1, 2, 3
 HCA_COMPRESS_NORM, HCA_COMPRESS_ROPE = 1, 2
 HCA_LAYER_CSA, HCA_LAYER_HCA, HCA_LAYER_SWA = 0, 1, 2
+HCA_W4_E2M1, HCA_W4_INT4 = 0, 1
 # HCA_STATIC_SCRATCH_BYTES of include/hca.h; lib() checks that the loaded library agrees.
 STATIC_SCRATCH_BYTES = 8 << 20
 
@@ -63,6 +64,23 @@ class Cache(C.Structure):
 class OprojDesc(C.Structure):
     _fields_ = [("T", C.c_int), ("n_h", C.c_int), ("c", C.c_int), ("g", C.c_int), ("d_g", C.c_int),
                 ("d", C.c_int), ("dtype", C.c_int), ("out_dtype", C.c_int)]
+
+
+class NormDesc(C.Structure):
+    _fields_ = [("rows", C.c_longlong), ("d", C.c_int), ("x_dtype", C.c_int), ("res_dtype", C.c_int),
+                ("out_dtype", C.c_int), ("scale_group", C.c_int), ("eps", C.c_float), ("ldx", C.c_longlong),
+                ("ldr", C.c_longlong), ("ldo", C.c_longlong)]
+
+
+class W4Desc(C.Structure):
+    _fields_ = [("T", C.c_int), ("N", C.c_int), ("K", C.c_int), ("groups", C.c_int), ("scale_group", C.c_int),
+                ("code", C.c_int), ("x_dtype", C.c_int), ("out_dtype", C.c_int), ("ldx", C.c_longlong),
+                ("ldo", C.c_longlong)]
+
+
+class Fp4Cache(C.Structure):
+    _fields_ = [("rows", C.c_void_p), ("cap", C.c_int), ("pages", C.c_void_p), ("max_pages", C.c_int),
+                ("n_pages", C.c_int)]
 
 
 class WsMap(C.Structure):
@@ -120,6 +138,15 @@ def _declare(L):
         "hybrid_cp_workspace_size": (SZ, [C.POINTER(Layer), I, I]),
         "hybrid_cp_compress": (I, [C.POINTER(Layer), VP, I, I, VP, VP, VP, I, VP, SZ, VP]),
         "hybrid_cp_attend": (I, [C.POINTER(Layer), VP, I, I, VP, VP, VP, I, VP, VP, SZ, VP]),
+        "hca_add_rms_norm": (I, [C.POINTER(NormDesc), VP, VP, VP, VP, VP, VP, VP]),
+        "hca_w4_linear_workspace_size": (SZ, [C.POINTER(W4Desc)]),
+        "hca_w4_linear": (I, [C.POINTER(W4Desc), VP, VP, VP, VP, VP, VP, VP, SZ, VP]),
+        "hca_w4_quantize": (I, [C.POINTER(W4Desc), VP, I, VP, VP, VP, VP]),
+        "hca_kv_fp4_row_bytes": (SZ, [I, I]),
+        "hca_kv_quant_fp4": (I, [VP, I, LL, I, I, VP, LL, VP, VP]),
+        "hca_kv_dequant_fp4": (I, [VP, LL, VP, LL, I, I, VP, VP]),
+        "hca_attend_fp4_workspace_size": (SZ, [C.POINTER(AttnDesc), I]),
+        "hca_attend_fp4": (I, [C.POINTER(AttnDesc), VP, C.POINTER(Fp4Cache), VP, VP, VP, VP, I, VP, VP, SZ, VP]),
         "hca_kv_quant_mixed": (I, [VP, I, LL, I, I, VP, VP]),
         "hca_kv_dequant_mixed": (I, [VP, LL, I, I, VP, VP]),
     }
@@ -425,3 +452,168 @@ def output_projection(d: OprojDesc, o, wo_a, wo_b, out, ws, stream=None):
     nbytes = ws.numel() * ws.element_size() if ws is not None else 0
     return check(lib().hca_output_projection(C.byref(d), ptr(o), ptr(wo_a), ptr(wo_b), ptr(out), ptr(ws), nbytes,
                                              stream_handle(stream)))
+
+
+# ------------------------------------------------------- the low-bit decode step
+# These calls take tensors only and check them (device, type, shape, layout)
+# before the library sees their addresses.
+def _bad(msg):
+    raise HcaError(HCA_ERR_INVALID, msg)
+
+
+_CODE_TYPES = {HCA_F32: (torch.float32,), HCA_BF16: (torch.bfloat16,),
+               HCA_FP8E4M3: (torch.float8_e4m3fn, torch.uint8)}
+_F32, _BF16, _U8, _I32, _I64 = ((t,) for t in (torch.float32, torch.bfloat16, torch.uint8, torch.int32, torch.int64))
+
+
+def _tensor(name, t, shape, types, ld=None):
+    """t on the current device, of one of the types and the shape; dense, or with rows ld elements apart."""
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        _bad(f"{name} must be on the current CUDA device (it is on {t.device})")
+    if t.dtype not in types:
+        _bad(f"{name} has dtype {t.dtype}, expected {types[0] if types else 'another'}")
+    if t.shape != shape:
+        _bad(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if ld is None or ld == shape[1]:
+        if not t.is_contiguous():
+            _bad(f"{name} must be contiguous")
+    elif (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) != ld):
+        _bad(f"{name} must have contiguous rows {ld} elements apart")
+    return t.data_ptr()
+
+
+def _scratch(ws):
+    """(address, bytes) of a workspace tensor, or of none."""
+    if ws is None:
+        return None, 0
+    return _tensor("ws", ws, ws.shape, (ws.dtype,)), ws.numel() * ws.element_size()
+
+
+def norm_desc(rows, d, x_dtype=HCA_BF16, res_dtype=None, out_dtype=HCA_BF16, scale_group=0, eps=1e-6, ldx=0, ldr=0,
+              ldo=0) -> NormDesc:
+    return NormDesc(rows, d, x_dtype, x_dtype if res_dtype is None else res_dtype, out_dtype, scale_group, eps, ldx,
+                    ldr, ldo)
+
+
+def add_rms_norm(d: NormDesc, x, res, gamma, res_out, out, out_scale=None, stream=None):
+    """out = RMSNorm(x + res) * gamma (e4m3 with out_scale, or bf16 / f32), res_out = x + res; see hca_add_rms_norm."""
+    shape = (d.rows, d.d)
+    px = _tensor("x", x, shape, _CODE_TYPES.get(d.x_dtype, ()), d.ldx or d.d)
+    rt = _CODE_TYPES.get(d.res_dtype, ())
+    pr = None if res is None else _tensor("res", res, shape, rt, d.ldr or d.d)
+    pro = None if res_out is None else _tensor("res_out", res_out, shape, rt, d.ldr or d.d)
+    pg = None if gamma is None else _tensor("gamma", gamma, (d.d,), _F32)
+    po = _tensor("out", out, shape, _CODE_TYPES.get(d.out_dtype, ()), d.ldo or d.d)
+    ps = None
+    if d.out_dtype == HCA_FP8E4M3:
+        if out_scale is None:
+            _bad("an e4m3 output needs out_scale")
+        ps = _tensor("out_scale", out_scale, (d.rows, d.d // d.scale_group if d.scale_group > 0 else 1), _F32)
+    return check(lib().hca_add_rms_norm(d, px, pr, pg, pro, po, ps, stream_handle(stream)))
+
+
+def w4_desc(T, N, K, groups=1, scale_group=32, code=HCA_W4_E2M1, x_dtype=HCA_BF16, out_dtype=HCA_BF16, ldx=0,
+            ldo=0) -> W4Desc:
+    return W4Desc(T, N, K, groups, scale_group, code, x_dtype, out_dtype, ldx, ldo)
+
+
+def w4_linear_workspace_size(d: W4Desc) -> int:
+    return lib().hca_w4_linear_workspace_size(d)
+
+
+def w4_linear(d: W4Desc, x, x_scale, codes, scales, row_scale, out, ws, stream=None):
+    """out = x @ W^T for 4-bit weights (w4_quantize) and T tokens; see hca_w4_linear."""
+    px = _tensor("x", x, (d.T, d.groups * d.K), _CODE_TYPES.get(d.x_dtype, ()), d.ldx or d.groups * d.K)
+    ps = None
+    if x_scale is not None:
+        if x_scale.dim() == 2:          # one scale per row as add_rms_norm writes them
+            x_scale = x_scale.view(-1)
+        ps = _tensor("x_scale", x_scale, (d.T,), _F32)
+    pc = _tensor("codes", codes, (d.groups * d.N, d.K // 2), _U8)
+    pw = _tensor("scales", scales, (d.groups, d.K // max(d.scale_group, 1), (d.N + 15) // 16 * 16),
+                 _CODE_TYPES[HCA_FP8E4M3])
+    pr = _tensor("row_scale", row_scale, (d.groups * d.N,), _F32)
+    po = _tensor("out", out, (d.T, d.groups * d.N), _CODE_TYPES.get(d.out_dtype, ()), d.ldo or d.groups * d.N)
+    pws, nws = _scratch(ws)
+    return check(lib().hca_w4_linear(d, px, ps, pc, pw, pr, po, pws, nws, stream_handle(stream)))
+
+
+def w4_quantize(d: W4Desc, w, stream=None):
+    """(codes, scales, row_scale) of weights w [groups*N, K], as w4_linear takes them."""
+    pw = _tensor("w", w, (d.groups * d.N, d.K), (torch.float32, torch.bfloat16))
+    codes = torch.empty(d.groups * d.N, d.K // 2, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(d.groups, d.K // max(d.scale_group, 1), (d.N + 15) // 16 * 16, dtype=torch.uint8,
+                         device=w.device)
+    row_scale = torch.empty(d.groups * d.N, dtype=torch.float32, device=w.device)
+    check(lib().hca_w4_quantize(d, pw, DTYPE_CODE[w.dtype], ptr(codes), ptr(scales), ptr(row_scale),
+                                stream_handle(stream)))
+    return codes, scales, row_scale
+
+
+def kv_fp4_row_bytes(c, rd) -> int:
+    """Bytes of one row's 4-bit record (0 = unsupported)."""
+    return lib().hca_kv_fp4_row_bytes(c, rd)
+
+
+def _fp4_records(name, t, c, rd):
+    rec = lib().hca_kv_fp4_row_bytes(c, rd)
+    if rec == 0:
+        _bad(f"unsupported (c, rd) = ({c}, {rd})")
+    return _tensor(name, t, t.shape[:-1] + (rec,), _U8), t.numel() // rec
+
+
+def kv_quant_fp4(x, c, rd, records, slots=None, stream=None):
+    """Rows x [rows, c] to 4-bit records: row r to record slots[r] (int64; r without slots)."""
+    po, n = _fp4_records("records", records, c, rd)
+    rows = x.shape[0]
+    px = _tensor("x", x, (rows, c), (torch.bfloat16, torch.float32))
+    ps = None if slots is None else _tensor("slots", slots, (rows,), _I64)
+    return check(lib().hca_kv_quant_fp4(px, DTYPE_CODE[x.dtype], rows, c, rd, po, n, ps, stream_handle(stream)))
+
+
+def kv_dequant_fp4(records, c, rd, out, slots=None, stream=None):
+    """4-bit records slots[r] (record r without slots) as bf16 rows out [rows, c]."""
+    pi, n = _fp4_records("records", records, c, rd)
+    rows = out.shape[0]
+    po = _tensor("out", out, (rows, c), _BF16)
+    ps = None if slots is None else _tensor("slots", slots, (rows,), _I64)
+    return check(lib().hca_kv_dequant_fp4(pi, n, ps, rows, c, rd, po, stream_handle(stream)))
+
+
+class Fp4CacheHandle:
+    """A cache of 4-bit records: rows [B, cap, rec], or with pages (int32
+    [B, max_pages]) rows [n_pages, cap, rec]; holds its tensors."""
+
+    def __init__(self, rows, cap, pages=None):
+        if rows.dim() != 3 or rows.shape[1] != cap:
+            _bad(f"rows must be [B or n_pages, cap, record bytes] with cap = {cap}")
+        if pages is not None and pages.dim() != 2:
+            _bad("pages must be [B, max_pages]")
+        self.rows, self.cap, self.pages = rows, cap, pages
+        self.struct = Fp4Cache(ptr(rows), cap, ptr(pages), 0 if pages is None else pages.shape[1], rows.shape[0])
+
+
+def fp4_cache(rows, cap, pages=None) -> Fp4CacheHandle:
+    return Fp4CacheHandle(rows, cap, pages)
+
+
+def attend_fp4_workspace_size(d: AttnDesc, max_pos) -> int:
+    return lib().hca_attend_fp4_workspace_size(C.byref(d), max_pos)
+
+
+def attend_fp4(d: AttnDesc, q, cache: Fp4CacheHandle, idx, kv_win, sink, positions, max_pos, o, ws, stream=None):
+    """Decode attention over a cache of 4-bit records, one position per sequence; see hca_attend_fp4."""
+    pq = _tensor("q", q, (d.B, d.n_h, d.c), _BF16)
+    po = _tensor("o", o, (d.B, d.n_h, d.c), _BF16)
+    _fp4_records("cache rows", cache.rows, d.c, d.rd)
+    if cache.pages is not None:
+        _tensor("pages", cache.pages, (d.B, cache.pages.shape[1]), _I32)
+    elif cache.rows.shape[0] != d.B:
+        _bad(f"the cache has {cache.rows.shape[0]} sequences, expected {d.B}")
+    pi = None if idx is None else _tensor("idx", idx, (d.B, d.k), _I32)
+    pk = None if kv_win is None else _tensor("kv_win", kv_win, (d.B, max(d.w, 1), d.c), _BF16)
+    ps = None if sink is None else _tensor("sink", sink, (d.n_h,), _F32)
+    pp = _tensor("positions", positions, (d.B,), _I32)
+    pws, nws = _scratch(ws)
+    return check(lib().hca_attend_fp4(d, pq, cache.struct, pi, pk, ps, pp, max_pos, po, pws, nws,
+                                      stream_handle(stream)))

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -207,6 +208,57 @@ struct AttendParams {
 };
 size_t attend_workspace_bytes(const AttendParams &p);
 int run_attend(const AttendParams &p, void *ws, size_t ws_bytes, cudaStream_t s);
+
+// ------------------------------------------------------------- low-bit decode
+struct NormParams {
+  long long rows, ldx, ldr, ldo;
+  int d, group;            // group: channels per e4m3 scale, 0 = the row
+  int vec;                 // every row of every tensor allows 8-channel accesses
+  float eps;
+  const void *x, *res;
+  const float *gamma;
+  void *res_out, *out;
+  float *out_scale;
+};
+int launch_add_rms_norm(const NormParams &p, hca_dtype xd, hca_dtype rd, hca_dtype od, cudaStream_t s);
+
+struct W4Params {
+  int T, N, K, groups, G, code, ldn;
+  long long ldx, ldo;
+  const void *x;
+  const float *x_scale;          // NULL: 1
+  const unsigned char *codes;    // [groups*N, K/2]
+  const unsigned char *scales;   // [groups, K/G, ldn] e4m3
+  const float *row_scale;        // [groups*N]
+  void *out, *ws;
+  int *status;
+};
+size_t w4_workspace_bytes(const W4Params &p);
+int launch_w4_linear(const W4Params &p, hca_dtype xd, hca_dtype od, cudaStream_t s);
+int launch_w4_quantize(const void *w, hca_dtype wd, const W4Params &p, void *codes, void *scales, float *row_scale,
+                       cudaStream_t s);
+
+size_t kv_fp4_row_bytes(int c, int rd);
+int launch_kv_quant_fp4(const void *x, hca_dtype dt, long long rows, int c, int rd, void *out, long long records,
+                        const long long *slots, cudaStream_t s);
+int launch_kv_dequant_fp4(const void *in, long long records, const long long *slots, long long rows, int c, int rd,
+                          void *out, cudaStream_t s);
+
+struct AttendFp4Params {
+  int B, n_h, c, rd, w, m, k, rec;
+  int cap, max_pages, n_pages;   // hca_fp4_cache
+  int max_pos, max_ctas;
+  float scale, theta;
+  double rope_freq[32];
+  const __nv_bfloat16 *q, *kv_win;
+  const unsigned char *rows;
+  const int32_t *pages, *idx, *positions;
+  const float *sink;             // NULL: none
+  __nv_bfloat16 *o;
+  int *status;
+};
+size_t attend_fp4_workspace_bytes(const AttendFp4Params &p);
+int run_attend_fp4(const AttendFp4Params &p, void *ws, size_t ws_bytes, cudaStream_t s);
 
 // ------------------------------------------------------------- GEMM / glue
 // C[M, N] = A[M, K] * B[N, K]^T (row-major, lda/ldb/ldc in elements).

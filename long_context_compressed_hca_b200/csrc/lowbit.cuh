@@ -1,0 +1,70 @@
+// lowbit.cuh -- device helpers of the low-bit decode kernels: E2M1 codes and
+// powers of two.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace hca {
+
+// Two f16 values (low half: low nibble) of one byte of E2M1 codes, by the
+// conversion instruction: exact.  Byte B of w.
+template <int B>
+__device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 x<4>;\n\t"
+      "mov.b32 {x0, x1, x2, x3}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, x%2;\n\t}"
+      : "=r"(r) : "r"(w), "n"(B));
+  return r;
+}
+// The eight values of one 32-bit word of E2M1 codes as f16 pairs.
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&r)[4]) {
+  r[0] = e2m1x2_f16x2<0>(w);
+  r[1] = e2m1x2_f16x2<1>(w);
+  r[2] = e2m1x2_f16x2<2>(w);
+  r[3] = e2m1x2_f16x2<3>(w);
+}
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+// e4m3 byte -> the f16 value in both halves (exact).
+__device__ __forceinline__ uint32_t e4m3_f16x2_dup(uint32_t b) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(b & 0xFFu), __NV_E4M3);
+  return (uint32_t)h.x * 0x10001u;
+}
+__device__ __forceinline__ float e4m3_f32(uint32_t b) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(b & 0xFFu), __NV_E4M3)));
+}
+__device__ __forceinline__ uint32_t f32_e4m3(float v) {   // nearest even, saturating; zero as +0
+  const uint32_t b = (uint32_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+  return (b & 0x7Fu) ? b : 0u;
+}
+
+// Nearest E2M1 code of v, ties to the even code, saturating at 6; zero as +0.
+// Codes k below 2 stand for k / 2, up to 4 for k - 2, above for 2 (k - 4):
+// rounding to the nearest even integer in each range ties to the even code.
+__device__ __forceinline__ uint32_t e2m1_code(float v) {
+  const float a = fminf(fabsf(v), 6.0f);
+  int k;
+  if (a < 2.0f) k = __float2int_rn(2.0f * a);
+  else if (a < 4.0f) k = __float2int_rn(a) + 2;
+  else k = min(__float2int_rn(0.5f * a) + 4, 7);
+  return k ? (uint32_t)k | (v < 0.f ? 8u : 0u) : 0u;
+}
+
+// 2^k, -126 <= k <= 127.
+__device__ __forceinline__ float pow2f(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+
+// The smallest e >= -126 with amax <= 6 * 2^e (amax finite, > 0): with amax =
+// f * 2^x, 1 <= f < 2, e = x - 2 for f <= 1.5 and x - 1 above.  A subnormal
+// amax has x = -127 here and ends at -126 either way.
+__device__ __forceinline__ int fp4_block_exp(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = (int)(u >> 23) - 127 - ((u & 0x7FFFFFu) > 0x400000u ? 1 : 2);
+  return max(e, -126);
+}
+
+}  // namespace hca
