@@ -97,8 +97,9 @@ int *device_status_ptr() {
   return ptr[dev];
 }
 
-int encode_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows,
-                   uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+namespace {
+int encode_tmap(CUtensorMap *map, const void *base, CUtensorMapDataType dt, int rank, const cuuint64_t *dims,
+                const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void *fn = nullptr;
@@ -107,15 +108,30 @@ int encode_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType dt, u
       return fail(HCA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {row_stride_bytes};
-  const cuuint32_t box[2] = {box_cols, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = encode(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr,
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = encode(map, dt, rank, const_cast<void *>(base), dims, strides, box, estr,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(HCA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return HCA_OK;
+}
+}  // namespace
+
+int encode_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows,
+                   uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {row_stride_bytes};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  return encode_tmap(map, base, dt, 2, dims, strides, box, swizzle);
+}
+
+int encode_tmap_3d(CUtensorMap *map, const void *base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows,
+                   uint64_t planes, uint64_t row_stride_bytes, uint64_t plane_stride_bytes, uint32_t box_cols,
+                   uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[3] = {cols, rows, planes};
+  const cuuint64_t strides[2] = {row_stride_bytes, plane_stride_bytes};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  return encode_tmap(map, base, dt, 3, dims, strides, box, swizzle);
 }
 
 int device_slot() {

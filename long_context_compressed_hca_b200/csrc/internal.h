@@ -44,6 +44,10 @@ int device_slot();
 int encode_tmap_2d(CUtensorMap *map, const void *base, CUtensorMapDataType dt, uint64_t cols,
                    uint64_t rows, uint64_t row_stride_bytes, uint32_t box_cols, uint32_t box_rows,
                    CUtensorMapSwizzle swizzle);
+// The same over `planes` such matrices plane_stride_bytes apart; the box covers one plane.
+int encode_tmap_3d(CUtensorMap *map, const void *base, CUtensorMapDataType dt, uint64_t cols, uint64_t rows,
+                   uint64_t planes, uint64_t row_stride_bytes, uint64_t plane_stride_bytes, uint32_t box_cols,
+                   uint32_t box_rows, CUtensorMapSwizzle swizzle);
 // Device address of the status word (HCA_OK or HCA_ERR_TIMEOUT) of the current device.
 int *device_status_ptr();
 

@@ -30,6 +30,16 @@ __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
+// Two f16 values of the two e4m3 bytes in the low half of w (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t hfma2_u32(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b),
+                            *reinterpret_cast<__half2 *>(&c));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
 // e4m3 byte -> the f16 value in both halves (exact).
 __device__ __forceinline__ uint32_t e4m3_f16x2_dup(uint32_t b) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(b & 0xFFu), __NV_E4M3);

@@ -88,7 +88,7 @@ int hca_add_rms_norm(const hca_norm_desc *d, const void *x, const void *res, con
 // ---------------------------------------------------------------- 4-bit weights
 size_t hca_w4_linear_workspace_size(const hca_w4_desc *d) {
   W4Params p;
-  if (w4_params(d, &p) || d->T < 0) return 0;
+  if (w4_params(d, &p) || d->T < 0 || (long long)d->groups * d->T > INT_MAX - 1024) return 0;
   p.T = d->T;
   return w4_workspace_bytes(p);
 }
@@ -98,7 +98,7 @@ int hca_w4_linear(const hca_w4_desc *d, const void *x, const float *x_scale, con
   W4Params p;
   const int rc = w4_params(d, &p);
   if (rc) return rc;
-  REQUIRE(d->T >= 0, "T must be >= 0");
+  REQUIRE(d->T >= 0 && (long long)d->groups * d->T <= INT_MAX - 1024, "T must be >= 0 and groups * T fit 31 bits");
   REQUIRE(d->x_dtype == HCA_BF16 || d->x_dtype == HCA_FP8E4M3, "x_dtype must be bf16 or e4m3");
   REQUIRE(d->out_dtype == HCA_F32 || d->out_dtype == HCA_BF16, "out_dtype must be f32 or bf16");
   p.T = d->T;
