@@ -65,6 +65,33 @@ __device__ __forceinline__ uint32_t e2m1_code(float v) {
   return k ? (uint32_t)k | (v < 0.f ? 8u : 0u) : 0u;
 }
 
+// Bounded wait as mbar_wait, limited by the SM's cycle counter: reading the
+// global timer on every wait that does not pass at once costs more than the
+// wait in a pipeline of a few hundred cycles per step.
+constexpr long long kWaitLimitCycles = 4000000000ll;   // about 2 s
+__device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, int *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      set_timeout_status(status);
+      return false;
+    }
+  }
+}
+
+// One lane of a converged warp.  A role that runs warp-uniform up to this
+// choice keeps MMA descriptors in uniform registers; one that runs on a lane
+// of its own moves each of them there again for every instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // 2^k, -126 <= k <= 127.
 __device__ __forceinline__ float pow2f(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 

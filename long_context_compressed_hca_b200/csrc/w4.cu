@@ -78,10 +78,14 @@ __global__ void __launch_bounds__(256) w4_x_kernel(W4Params p, __half *xh, float
 // is the list of (tile, 256-channel unit) pairs; every CTA takes an equal run
 // of it, so that HBM is read evenly whatever the tile count, and a tile cut
 // between CTAs is joined from fp32 parts in a fixed order by w4_join_kernel.
-// Roles: warp 0 streams codes, scales and x by TMA; warps 2-9 turn codes into
-// f16 weights, a thread per output row, and write them to tensor memory as
-// the A operand (no shared-memory round trip); warp 1 issues the MMAs; warps
-// 10-13 read finished accumulators while the next tile's run.
+// Roles: warp 0 streams codes and scales by TMA, another warp x; 16 warps turn
+// codes into f16 weights, a thread per output row and quarter of a unit, and
+// write them to tensor memory as the A operand (no shared-memory round trip);
+// two warps issue the MMAs, each of one half of every unit's channels into an
+// accumulator of its own; four warps add the two and store.  A unit is a chain
+// of waits, MMAs and commits in its issuing warp (about 1000 cycles for 16
+// MMAs, of which the tensor pipe works 512 at 64 tokens), hence the two: 64
+// tokens x 28677 x 8192 took 56 us with one.
 struct W4Work {
   int nk, nb, ntt, G;      // units per tile, output blocks, token tiles, CTAs
   long long U;             // units of all tiles
@@ -120,18 +124,31 @@ W4Ws w4_ws(const W4Params &p) {
   return l;
 }
 
+// Tensor memory: 128 columns of accumulators -- up to 32 tokens two pairs, so
+// that one is stored while the other fills; at 64 tokens one pair -- then the
+// buffers of decoded weights, 128 columns each.
+constexpr int kNA = 3;
+constexpr uint32_t kACol = 128;
+
 template <int TN>
 struct W4Layout {
+  // Codes and x have rings of their own: a stage of codes is free once it has
+  // been decoded, x stays until its MMAs have run.  Both sizes cover the time
+  // from a load's issue to its use: 64 tokens x 28677 x 8192 took 58 us with
+  // one ring of 4 stages for both, 54 with 7 of codes and 3 of x.
   static constexpr uint32_t kCodes = kTileN * 128, kX = 4 * TN * 128, kScales = 8 * 128;
-  static constexpr uint32_t kStage = kCodes + kX + kScales;
-  static constexpr int NST = TN == 64 ? 4 : TN == 32 ? 6 : 8;
-  static constexpr uint32_t bar_off = NST * kStage;
-  static constexpr uint32_t bytes = bar_off + 256 + 1024;
+  static constexpr uint32_t kStage = kCodes + kScales;
+  static constexpr int NC = TN == 64 ? 5 : TN == 32 ? 7 : 9, NX = TN == 64 ? 4 : TN == 32 ? 6 : 8;
+  static constexpr int ND = TN == 64 ? 1 : 2;
+  static constexpr uint32_t kSecond = TN == 64 ? 64 : 32;   // column of the second accumulator in its pair
+  static constexpr uint32_t x_off = NC * kStage;
+  static constexpr uint32_t bar_off = x_off + NX * kX;
+  static constexpr uint32_t bytes = bar_off + 512 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory");
 };
-constexpr int kNA = 3;                   // A buffers in tensor memory, 128 columns each, behind two accumulators of 64
-constexpr uint32_t kACol = 128;
-constexpr int kW4Threads = 14 * 32;
+constexpr int kDecWarps = 16, kEpi0 = 2 + kDecWarps;     // first epilogue warp
+constexpr int kXWarp = kEpi0 + 4, kMma1 = kEpi0 + 5;    // x loads; MMAs of the second half (warp 1: of the first)
+constexpr int kW4Threads = (kMma1 + 1) * 32;
 
 // 32 codes of a 16-byte chunk as 16 f16 pairs, times the scale s2 (t2: INT4's offset).
 template <int CODE>
@@ -166,24 +183,29 @@ __global__ void __launch_bounds__(kW4Threads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   struct Bars {
-    uint64_t full[L::NST], empty[L::NST], a_full[kNA], a_empty[kNA], d_full[2], d_empty[2];
+    uint64_t c_full[L::NC], c_empty[L::NC], x_full[L::NX], x_empty[L::NX], a_full[2][kNA], a_empty[2][kNA], d_full[2],
+        d_empty[2];
     uint32_t tmem;
   };
-  static_assert(sizeof(Bars) <= 256, "barriers");
+  static_assert(sizeof(Bars) <= 512, "barriers");
   Bars *bars = reinterpret_cast<Bars *>(smem + L::bar_off);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   auto bar = [&](uint64_t &b) { return smem_u32(&b); };
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::NST; ++i) {
-      mbar_init(bar(bars->full[i]), 1);
-      mbar_init(bar(bars->empty[i]), 9);       // 8 weight warps and the MMAs' commit
+    for (int i = 0; i < L::NC; ++i) {
+      mbar_init(bar(bars->c_full[i]), 1);
+      mbar_init(bar(bars->c_empty[i]), kDecWarps);
     }
-    for (int i = 0; i < kNA; ++i) {
-      mbar_init(bar(bars->a_full[i]), 8);
-      mbar_init(bar(bars->a_empty[i]), 1);
+    for (int i = 0; i < L::NX; ++i) {
+      mbar_init(bar(bars->x_full[i]), 1);
+      mbar_init(bar(bars->x_empty[i]), 2);
+    }
+    for (int i = 0; i < 2 * kNA; ++i) {
+      mbar_init(bar(bars->a_full[i / kNA][i % kNA]), kDecWarps / 2);
+      mbar_init(bar(bars->a_empty[i / kNA][i % kNA]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(bars->d_full[i]), 1);
+      mbar_init(bar(bars->d_full[i]), 2);
       mbar_init(bar(bars->d_empty[i]), 4);
     }
     mbar_fence_init();
@@ -195,156 +217,180 @@ __global__ void __launch_bounds__(kW4Threads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
   const long long u0 = wk.lo(blockIdx.x), u1 = wk.lo(blockIdx.x + 1);
   const int n = (int)(u1 - u0);
   pdl_trigger();
 
-  if (warp == 0) {
+  if (warp == 0 || warp == kXWarp) {
     if (lane == 0) {
-      tma_prefetch_desc(&tmC);
-      tma_prefetch_desc(&tmS);
-      tma_prefetch_desc(&tmX);
-      const uint32_t bytes = L::kCodes + L::kX + (uint32_t)(kBlk / p.G) * 128u;
-      auto where = [&](int i, int &k, int &n0, int &g, int &row) {
-        const long long u = u0 + i, tile = u / wk.nk;
-        k = (int)(u - tile * wk.nk) * kBlk;
-        // token tiles innermost: the CTAs of one weight block run together
+      // walks the units: the tile's place is worked out once per tile (64-bit
+      // divisions on every unit would cost the one issuing thread more than
+      // the unit's time)
+      long long tile = u0 / wk.nk;
+      int kb = (int)(u0 - tile * wk.nk), n0, g, row;
+      auto place = [&]() {   // token tiles innermost: the CTAs of one weight block run together
         const long long blk = tile / wk.ntt;
         g = (int)(blk / wk.nb);
         n0 = (int)(blk - (long long)g * wk.nb) * kTileN;
         row = g * p.T + (int)(tile - blk * wk.ntt) * TN;
       };
-      auto load_w = [&](int i, int st) {
-        int k, n0, g, row;
-        where(i, k, n0, g, row);
-        const uint32_t b = bar(bars->full[st]), a = sbase + st * L::kStage;
-        mbar_arrive_expect_tx(b, bytes);
-        tma_load_3d(a, &tmC, k / 2, n0, g, b);
-        tma_load_3d(a + L::kCodes + L::kX, &tmS, n0, k / p.G, g, b);
-      };
-      auto load_x = [&](int i, int st) {
-        int k, n0, g, row;
-        where(i, k, n0, g, row);
-        const uint32_t b = bar(bars->full[st]), a = sbase + st * L::kStage + L::kCodes;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tma_load_2d(a + j * TN * 128, &tmX, k + 64 * j, row, b);
-      };
-      // the weights of the first stages do not depend on the kernel that writes x
-      const int pre = min(n, L::NST);
-      for (int i = 0; i < pre; ++i) load_w(i, i);
-      pdl_wait();
-      for (int i = 0; i < pre; ++i) load_x(i, i);
-      for (int i = pre; i < n; ++i) {
-        const int st = i % L::NST;
-        if (!mbar_wait_sleep(bar(bars->empty[st]), ((i / L::NST) & 1) ^ 1, p.status)) break;
-        load_w(i, st);
-        load_x(i, st);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t IDESC = idesc_f16(128, TN);
-      int d = 0, dph = 0;                       // accumulator and its phase
-      int kb = (int)(u0 % wk.nk);
-      bool first = true;
-      for (int i = 0; i < n; ++i) {
-        const int st = i % L::NST, ab = i % kNA;
-        if (!mbar_wait(bar(bars->full[st]), (i / L::NST) & 1, p.status)) break;
-        if (!mbar_wait(bar(bars->a_full[ab]), (i / kNA) & 1, p.status)) break;
-        if (first && !mbar_wait(bar(bars->d_empty[d]), dph ^ 1, p.status)) break;
-        tc_fence_after();
-        const uint64_t xdesc = sdesc_sw128(sbase + st * L::kStage + L::kCodes, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < kBlk / 16; ++kk)
-          umma_bf16_ts(tmem + d * 64, tmem + kACol + ab * 128 + 8 * kk,
-                       xdesc + (((kk / 4) * TN * 128 + (kk % 4) * 32) >> 4), IDESC, first && kk == 0 ? 0u : 1u);
-        umma_commit(bar(bars->a_empty[ab]));
-        umma_commit(bar(bars->empty[st]));
-        first = false;
-        if (++kb == wk.nk || i == n - 1) {
-          umma_commit(bar(bars->d_full[d]));
+      auto next = [&]() {
+        if (++kb == wk.nk) {
           kb = 0;
-          first = true;
-          d ^= 1;
-          dph ^= d == 0;
+          ++tile;
+          place();
+        }
+      };
+      place();
+      if (warp == 0) {
+        // the weights do not depend on the kernel that writes x
+        tma_prefetch_desc(&tmC);
+        tma_prefetch_desc(&tmS);
+        const uint32_t bytes = L::kCodes + (uint32_t)(kBlk / p.G) * 128u;
+        const int sshift = p.G == 32 ? 3 : p.G == 64 ? 2 : 1;   // scale rows of a unit: 2^sshift
+        for (int i = 0; i < n; ++i, next()) {
+          const int st = i % L::NC;
+          if (!mbar_wait_fast(bar(bars->c_empty[st]), ((i / L::NC) & 1) ^ 1, p.status)) break;
+          const uint32_t b = bar(bars->c_full[st]), a = sbase + st * L::kStage;
+          mbar_arrive_expect_tx(b, bytes);
+          tma_load_3d(a, &tmC, kb * (kBlk / 2), n0, g, b);
+          tma_load_3d(a + L::kCodes, &tmS, n0, kb << sshift, g, b);
+        }
+      } else {
+        tma_prefetch_desc(&tmX);
+        pdl_wait();
+        for (int i = 0; i < n; ++i, next()) {
+          const int st = i % L::NX;
+          if (!mbar_wait_fast(bar(bars->x_empty[st]), ((i / L::NX) & 1) ^ 1, p.status)) break;
+          const uint32_t b = bar(bars->x_full[st]), a = sbase + L::x_off + st * L::kX;
+          mbar_arrive_expect_tx(b, L::kX);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tma_load_2d(a + j * TN * 128, &tmX, kb * kBlk + 64 * j, row, b);
         }
       }
     }
     __syncwarp();
-  } else if (warp < 10) {
-    // weights: row r of the tile, 16-byte chunks [4 half, 4 half + 4) of the stage's 8
-    const int q = warp & 3, half = (warp - 2) >> 2, r = q * 32 + lane;
-    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + kACol;
+  } else if (warp == 1 || warp == kMma1) {
+    constexpr uint32_t IDESC = idesc_f16(128, TN);
+    const int half = warp == 1 ? 0 : 1;
+    const uint64_t xdesc0 = sdesc_sw128(sbase + L::x_off, 16, 1024) + ((half * 2 * TN * 128) >> 4);
+    int ab = 0, xs = 0, left = wk.nk - (int)(u0 % wk.nk);   // left: units of the tile
+    uint32_t aph = 0, xph = 0;
+    bool ok = true;
+    for (int i = 0, piece = 0; i < n && ok; ++piece) {
+      const int end = min(n, i + left), d = piece % L::ND;   // units [i, end) of one tile
+      left = wk.nk;
+      ok = mbar_wait_fast(bar(bars->d_empty[d]), ((piece / L::ND) & 1) ^ 1, p.status);
+      const uint32_t td = tmem + d * 64 + half * L::kSecond;
+      for (uint32_t acc = 0; i < end && ok; ++i, acc = 1) {
+        ok = mbar_wait_fast(bar(bars->x_full[xs]), xph, p.status) &&
+             mbar_wait_fast(bar(bars->a_full[half][ab]), aph, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t xdesc = xdesc0 + xs * (L::kX >> 4);
+          const uint32_t ta = tmem + kACol + ab * 128 + half * 64;
+#pragma unroll
+          for (int kk = 0; kk < kBlk / 32; ++kk)
+            umma_bf16_ts(td, ta + 8 * kk, xdesc + (((kk / 4) * TN * 128 + (kk % 4) * 32) >> 4), IDESC,
+                         kk > 0 ? 1u : acc);
+          umma_commit(bar(bars->a_empty[half][ab]));
+          umma_commit(bar(bars->x_empty[xs]));
+          if (i + 1 == end) umma_commit(bar(bars->d_full[d]));
+        }
+        __syncwarp();
+        if (++ab == kNA) {
+          ab = 0;
+          aph ^= 1;
+        }
+        if (++xs == L::NX) {
+          xs = 0;
+          xph ^= 1;
+        }
+      }
+    }
+  } else if (warp < kEpi0) {
+    // weights: row r of the tile, 16-byte chunks 2 kq and 2 kq + 1 of the stage's 8
+    const int q = warp & 3, kq = (warp - 2) >> 2, r = q * 32 + lane;
+    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + kACol + kq * 32;
     const int gsh = p.G == 32 ? 0 : p.G == 64 ? 1 : 2;
+    const uint32_t o0 = r * 128 + (((2 * kq) ^ (r & 7)) << 4), o1 = r * 128 + (((2 * kq + 1) ^ (r & 7)) << 4);
+    const uint32_t s0 = L::kCodes + ((2 * kq) >> gsh) * 128 + r, s1 = L::kCodes + ((2 * kq + 1) >> gsh) * 128 + r;
+    int st = 0, ab = 0;
+    uint32_t cph = 0, aph = 1;
     for (int i = 0; i < n; ++i) {
-      const int st = i % L::NST, ab = i % kNA;
-      if (!mbar_wait(bar(bars->full[st]), (i / L::NST) & 1, p.status)) break;
-      const uint8_t *codes = smem + st * L::kStage + r * 128;
-      const uint8_t *sc = smem + st * L::kStage + L::kCodes + L::kX + r;
-      uint4 v[4];
-      uint32_t s2[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        v[c] = *reinterpret_cast<const uint4 *>(codes + (((4 * half + c) ^ (r & 7)) << 4));
-        s2[c] = sc[((4 * half + c) >> gsh) * 128];
-      }
+      if (!mbar_wait_fast(bar(bars->c_full[st]), cph, p.status)) break;
+      const uint8_t *stage = smem + st * L::kStage;
+      const uint4 v0 = *reinterpret_cast<const uint4 *>(stage + o0), v1 = *reinterpret_cast<const uint4 *>(stage + o1);
+      const uint32_t sa = e4m3_f16x2_dup(stage[s0]), sb = e4m3_f16x2_dup(stage[s1]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(bars->empty[st]));
-      if (!mbar_wait(bar(bars->a_empty[ab]), ((i / kNA) & 1) ^ 1, p.status)) break;
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t s = e4m3_f16x2_dup(s2[c]);
-        uint32_t t = 0;
-        if constexpr (CODE == HCA_W4_INT4) t = hmul2_u32(s, 0xA400A400u);   // -2^-6: -8 of the byte's units
-        uint32_t f[16];
-        w4_decode<CODE>(v[c], s, t, f);
-        tmem_st_32x32b_x16(ta + ab * 128 + (4 * half + c) * 16, f);
+      if (lane == 0) mbar_arrive(bar(bars->c_empty[st]));
+      uint32_t na = 0, nb = 0;
+      if constexpr (CODE == HCA_W4_INT4) {   // times -2^-6: -8 of the byte's units
+        na = hmul2_u32(sa, 0xA400A400u);
+        nb = hmul2_u32(sb, 0xA400A400u);
       }
+      uint32_t f0[16], f1[16];
+      w4_decode<CODE>(v0, sa, na, f0);
+      w4_decode<CODE>(v1, sb, nb, f1);
+      if (!mbar_wait_fast(bar(bars->a_empty[kq >> 1][ab]), aph, p.status)) break;
+      tc_fence_after();
+      tmem_st_32x32b_x16(ta + ab * 128, f0);
+      tmem_st_32x32b_x16(ta + ab * 128 + 16, f1);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(bars->a_full[ab]));
+      if (lane == 0) mbar_arrive(bar(bars->a_full[kq >> 1][ab]));
+      if (++st == L::NC) {
+        st = 0;
+        cph ^= 1;
+      }
+      if (++ab == kNA) {
+        ab = 0;
+        aph ^= 1;
+      }
     }
   } else {
+    // finished accumulators
     pdl_wait();   // xd of the kernel before
     const int q = warp & 3, f = q * 32 + lane;
     const uint32_t td = tmem + ((uint32_t)(q * 32) << 16);
-    int d = 0, dph = 0;
-    for (long long u = u0; u < u1;) {
+    int piece = 0;
+    for (long long u = u0; u < u1; ++piece) {
+      const int d = piece % L::ND;
       const long long tile = u / wk.nk, end = min((tile + 1) * wk.nk, u1);
       const bool whole = u == tile * wk.nk && end == (tile + 1) * wk.nk;
+      const uint32_t tp = td + d * 64;
       const long long blk = tile / wk.ntt;
       const int g = (int)(blk / wk.nb), o = (int)(blk - (long long)g * wk.nb) * kTileN + f;
       const int t0 = (int)(tile - blk * wk.ntt) * TN, nt = min(TN, p.T - t0);
       float rs = 0.f;
       if (whole && o < p.N) rs = p.row_scale[(long long)g * p.N + o] * (CODE == HCA_W4_INT4 ? 512.f : 1.f);
-      if (!mbar_wait(bar(bars->d_full[d]), dph, p.status)) break;
+      if (!mbar_wait_fast(bar(bars->d_full[d]), (piece / L::ND) & 1, p.status)) break;
       tc_fence_after();
       float *pp = part + (long long)wk.slot(blockIdx.x, tile) * min(TN, p.T) * kTileN + f;
 #pragma unroll 1
       for (int j0 = 0; j0 < nt; j0 += 16) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(td + d * 64 + j0, v);
+        uint32_t v[16], v1[16];
+        tmem_ld_32x32b_x16(tp + j0, v);
+        tmem_ld_32x32b_x16(tp + L::kSecond + j0, v1);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int t = j0 + j;
           if (t < nt) {
-            if (!whole) pp[t * kTileN] = __uint_as_float(v[j]);
+            const float a = __uint_as_float(v[j]) + __uint_as_float(v1[j]);
+            if (!whole) pp[t * kTileN] = a;
             else if (o < p.N)
               Elt<OT>::store(static_cast<OT *>(p.out) + (long long)(t0 + t) * p.ldo + (long long)g * p.N + o,
-                             __uint_as_float(v[j]) * rs * xd[g * p.T + t0 + t]);
+                             a * rs * xd[g * p.T + t0 + t]);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars->d_empty[d]));
-      d ^= 1;
-      dph ^= d == 0;
       u = end;
     }
   }
