@@ -32,6 +32,8 @@ int w4_params(const hca_w4_desc *d, W4Params *p) {
   REQUIRE(d->code == HCA_W4_E2M1 || d->code == HCA_W4_INT4, "code must be HCA_W4_E2M1 or HCA_W4_INT4");
   REQUIRE((long long)d->groups * d->N <= INT_MAX - 1024 && (long long)d->groups * d->K <= INT_MAX - 1024,
           "groups * N and groups * K must fit 31 bits");
+  REQUIRE((long long)d->groups * ((d->N + 127) / 128) * ((d->K + 255) / 256) <= INT_MAX / 64,
+          "groups * N * K is too large");
   *p = W4Params{};
   p->N = d->N; p->K = d->K; p->groups = d->groups; p->G = d->scale_group; p->code = d->code;
   p->ldn = (d->N + 15) / 16 * 16;

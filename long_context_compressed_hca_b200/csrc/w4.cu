@@ -21,6 +21,36 @@ namespace {
 constexpr int kBlk = 256;        // channels of one work unit (one pipeline stage)
 constexpr int kTileN = 128;      // outputs of one tile: the MMA's M
 
+// ---------------------------------------------------------------- codes
+// Eight codes as f16 pairs in the order of their channels, times the scale s2
+// (INT4: t2 = -8 units of it).
+template <int CODE>
+__device__ __forceinline__ void w4_decode8(uint32_t w, uint32_t s2, uint32_t t2, uint32_t *r) {
+  if constexpr (CODE == HCA_W4_E2M1) {
+    uint32_t f[4];
+    e2m1x8_f16(w, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = hmul2_u32(f[j], s2);
+  } else {
+    // u = code + 8 in 0..15 read as an e4m3 byte is u 2^-9 (subnormals, then exponent 1): the value
+    // (u - 8) 2^-9 s by one fused multiply-add, exact; the 2^9 is in the epilogue's factor
+    const uint32_t u = w ^ 0x88888888u, a = u & 0x0F0F0F0Fu, d = (u >> 4) & 0x0F0F0F0Fu;
+    const uint32_t lo = __byte_perm(a, d, 0x5140), hi = __byte_perm(a, d, 0x7362);
+    r[0] = hfma2_u32(e4m3x2_f16x2(lo), s2, t2);
+    r[1] = hfma2_u32(e4m3x2_f16x2(lo >> 16), s2, t2);
+    r[2] = hfma2_u32(e4m3x2_f16x2(hi), s2, t2);
+    r[3] = hfma2_u32(e4m3x2_f16x2(hi >> 16), s2, t2);
+  }
+}
+// The 32 of a 16-byte chunk.
+template <int CODE>
+__device__ __forceinline__ void w4_decode(const uint4 &q, uint32_t s2, uint32_t t2, uint32_t (&r)[16]) {
+  w4_decode8<CODE>(q.x, s2, t2, r);
+  w4_decode8<CODE>(q.y, s2, t2, r + 4);
+  w4_decode8<CODE>(q.z, s2, t2, r + 8);
+  w4_decode8<CODE>(q.w, s2, t2, r + 12);
+}
+
 // ---------------------------------------------------------------- x in f16
 // Row (g, t) of the workspace: K f16 values, zeros up to Kp, and the factor
 // that the sum over them is multiplied by.
@@ -73,6 +103,215 @@ __global__ void __launch_bounds__(256) w4_x_kernel(W4Params p, __half *xh, float
   }
 }
 
+// ---------------------------------------------------------------- few tokens
+// One launch and no workspace when x of all tokens fits in shared memory: a
+// block stages it as f16 (scaled as above; the block holds whole rows, so it
+// finds their maxima itself) and its 8 warps multiply 16 MT weight rows each
+// by mma.sync with the decoded codes as the A fragment, read from global
+// memory where they are needed.  The order of the channels inside an MMA is
+// free as long as A and B agree: lane t of a quad holds 32 successive ones of
+// 128, 16 bytes of codes.  With few rows KS warps share them, each with a part
+// of the channels, and are added in a fixed order.
+// Against the kernel below (its three launches and pipeline fill): 1 x 512 x
+// 4096 12.1 us -> see kFewElems.
+constexpr int kFewWarps = 8;
+constexpr int kFewElems = 96 * 1024;    // staged values: 192 KB
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Staged row pitch in bytes: 128-byte multiples plus 32, so that the 16-byte
+// reads of 2 tokens x 4 quad lanes fall into different banks.
+__host__ __device__ constexpr int few_pitch(int Kp) { return Kp * 2 + 32; }
+
+template <int MT, int NT, int CODE, typename XT, typename OT>
+__global__ void __launch_bounds__(kFewWarps * 32, 2) w4_few_kernel(W4Params p, int KS, int Kp) {
+  extern __shared__ __align__(16) uint8_t sm[];
+  __shared__ float xd[8 * NT];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.y;
+  const int t = lane & 3, gr = lane >> 2;
+  const int ks = warp % KS, rb = warp / KS;
+  const int row0 = (blockIdx.x * (kFewWarps / KS) + rb) * 16 * MT;
+  const int nblk = Kp / 128, b0 = (int)((long long)ks * nblk / KS), b1 = (int)((long long)(ks + 1) * nblk / KS);
+  const int pitch = few_pitch(Kp);
+
+  // this lane's 16 bytes of block b for row `row0 + 16 m + gr + 8 h`
+  const int nrow[2] = {row0 + gr, row0 + gr + 8};
+  auto load = [&](int b, uint4 (&v)[MT][2], uint32_t (&sc)[MT][2]) {
+    const int k = b * 128 + 32 * t;
+    const bool in = k < p.K;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = nrow[h] + 16 * m;
+        const bool on = in && r < p.N;
+        v[m][h] = on ? __ldg(reinterpret_cast<const uint4 *>(p.codes + ((long long)g * p.N + r) * (p.K / 2) + k / 2))
+                     : make_uint4(0, 0, 0, 0);
+        sc[m][h] = on ? __ldg(p.scales + ((long long)g * (p.K / p.G) + k / p.G) * p.ldn + r) : 0u;
+      }
+  };
+  // PF blocks of codes are on their way at a time, the first of them while x is staged
+  constexpr int PF = MT == 1 ? 4 : 2;
+  uint4 v[PF][MT][2];
+  uint32_t sc[PF][MT][2];
+#pragma unroll
+  for (int u = 0; u < PF; ++u)
+    if (b0 + u < b1) load(b0 + u, v[u], sc[u]);
+
+  // ---- x of all tokens as f16; rows of tokens beyond the last are zero
+  const int per = Kp / 8, tot = p.T * per;               // 8-value chunks, a multiple of 16 per token
+  for (int c = tot + tid; c < 8 * NT * per; c += kFewWarps * 32) {
+    const int tk = c / per;
+    *reinterpret_cast<uint4 *>(sm + tk * pitch + 16 * (c - tk * per)) = make_uint4(0, 0, 0, 0);
+  }
+  if constexpr (sizeof(XT) == 1) {
+#pragma unroll 4
+    for (int c = tid; c < tot; c += kFewWarps * 32) {
+      const int tk = c / per, k = 8 * (c - tk * per);
+      const XT *x = static_cast<const XT *>(p.x) + (long long)tk * p.ldx + (long long)g * p.K + k;
+      const uint2 u = k < p.K ? *reinterpret_cast<const uint2 *>(x) : make_uint2(0, 0);
+      *reinterpret_cast<uint4 *>(sm + tk * pitch + 2 * k) =
+          make_uint4(e4m3x2_f16x2(u.x), e4m3x2_f16x2(u.x >> 16), e4m3x2_f16x2(u.y), e4m3x2_f16x2(u.y >> 16));
+    }
+    if (tid < p.T) xd[tid] = p.x_scale[tid];
+  } else {
+    // the bf16 values first, then in place once each token's largest is known
+    __shared__ uint32_t amax[8 * NT];                     // |x| as bits, in the order of the values
+    if (tid < 8 * NT) amax[tid] = 0u;
+    __syncthreads();
+#pragma unroll 8
+    for (int c = tid; c < tot; c += kFewWarps * 32) {
+      const int tk = c / per, k = 8 * (c - tk * per);
+      const XT *x = static_cast<const XT *>(p.x) + (long long)tk * p.ldx + (long long)g * p.K + k;
+      const uint4 u = k < p.K ? *reinterpret_cast<const uint4 *>(x) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4 *>(sm + tk * pitch + 2 * k) = u;
+      uint32_t am = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                             __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+      am = max(am & 0xFFFFu, am >> 16);
+      am = __reduce_max_sync(0xFFFFu << (lane & 16), am);   // 16 lanes of one token
+      if ((lane & 15) == 0) atomicMax(&amax[tk], am);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int c = tid; c < tot; c += kFewWarps * 32) {
+      const int tk = c / per, k = 8 * (c - tk * per);
+      // 2^e <= the largest value < 2^(e + 1), e at least -110 so that 2^(14 - e) and its inverse are normal
+      const float up = pow2f(14 - max((int)(amax[tk] >> 7) - 127, -110));
+      uint8_t *o = sm + tk * pitch + 2 * k;
+      float f[8];
+      load8(reinterpret_cast<const __nv_bfloat16 *>(o), f);
+      __half2 h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i] * up, f[2 * i + 1] * up);
+      *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(h);
+    }
+    if (tid < p.T) xd[tid] = pow2f(max((int)(amax[tid] >> 7) - 127, -110) - 14);
+  }
+  __syncthreads();
+
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
+
+  auto multiply = [&](int b, const uint4 (&v)[MT][2], const uint32_t (&sc)[MT][2]) {
+    uint32_t s2[MT][2], t2[MT][2], w[MT][2][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s2[m][h] = e4m3_f16x2_dup(sc[m][h]);
+        t2[m][h] = CODE == HCA_W4_INT4 ? hmul2_u32(s2[m][h], 0xA400A400u) : 0u;
+        // lanes 2 and 3 of a quad take their words in pairwise swapped order: with it the four lanes'
+        // reads of x fall into four different 16-byte bank groups
+        const uint4 &q = v[m][h];
+        w[m][h][0] = t & 2 ? q.y : q.x;
+        w[m][h][1] = t & 2 ? q.x : q.y;
+        w[m][h][2] = t & 2 ? q.w : q.z;
+        w[m][h][3] = t & 2 ? q.z : q.w;
+      }
+    const uint8_t *xb = sm + gr * pitch + (b * 128 + 32 * t) * 2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = j ^ (t >> 1);
+      uint4 xv[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) xv[n] = *reinterpret_cast<const uint4 *>(xb + n * 8 * pitch + 16 * c);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t f[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w4_decode8<CODE>(w[m][h][j], s2[m][h], t2[m][h], f[h]);
+        const uint32_t a0[4] = {f[0][0], f[1][0], f[0][1], f[1][1]}, a1[4] = {f[0][2], f[1][2], f[0][3], f[1][3]};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_f16(acc[m][n], a0, xv[n].x, xv[n].y);
+          mma_f16(acc[m][n], a1, xv[n].z, xv[n].w);
+        }
+      }
+    }
+  };
+  for (int b = b0; b < b1; b += PF) {
+#pragma unroll
+    for (int u = 0; u < PF; ++u) {
+      if (b + u >= b1) break;
+      multiply(b + u, v[u], sc[u]);
+      if (b + u + PF < b1) load(b + u + PF, v[u], sc[u]);
+    }
+  }
+
+  // ---- parts of the KS warps of one row set, added in order
+  if (KS > 1) {
+    __syncthreads();                       // x has been read
+    float *red = reinterpret_cast<float *>(sm) + warp * (MT * NT * 128);
+    if (ks > 0) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          *reinterpret_cast<float4 *>(red + (m * NT + j) * 128 + 4 * lane) =
+              make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
+    }
+    __syncthreads();
+    if (ks > 0) return;
+    for (int z = 1; z < KS; ++z)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float4 a = *reinterpret_cast<const float4 *>(red + z * (MT * NT * 128) + (m * NT + j) * 128 + 4 * lane);
+          acc[m][j][0] += a.x; acc[m][j][1] += a.y; acc[m][j][2] += a.z; acc[m][j][3] += a.w;
+        }
+  }
+  // accumulator i: row gr + 8 (i / 2), token 2 t + i % 2
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = nrow[h] + 16 * m;
+      if (r >= p.N) continue;
+      const float rs = __ldg(p.row_scale + (long long)g * p.N + r) * (CODE == HCA_W4_INT4 ? 512.f : 1.f);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int tk = 8 * j + 2 * t + i;
+          if (tk < p.T)
+            Elt<OT>::store(static_cast<OT *>(p.out) + (long long)tk * p.ldo + (long long)g * p.N + r,
+                           acc[m][j][2 * h + i] * rs * xd[tk]);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- the product
 // Outputs are the MMA's M (128 per tile), tokens its N (TN <= 64).  The work
 // is the list of (tile, 256-channel unit) pairs; every CTA takes an equal run
@@ -86,27 +325,55 @@ __global__ void __launch_bounds__(256) w4_x_kernel(W4Params p, __half *xh, float
 // of waits, MMAs and commits in its issuing warp (about 1000 cycles for 16
 // MMAs, of which the tensor pipe works 512 at 64 tokens), hence the two: 64
 // tokens x 28677 x 8192 took 56 us with one.
+//
+// x reaches shared memory in one of two ways.  Where a block needs few units
+// of it (kByUnit: its run has at most NX; kByBlock: one group whose rows have
+// at most NX) the weight warps stage it themselves at the start, while the
+// first codes are on their way, and it stays (no kernel before this one, no
+// ring).  Otherwise w4_x_kernel writes it to the workspace and a warp streams
+// it by TMA.
+enum W4X { kRing = 0, kByUnit = 1, kByBlock = 2 };
 struct W4Work {
   int nk, nb, ntt, G;      // units per tile, output blocks, token tiles, CTAs
-  long long U;             // units of all tiles
-  __host__ __device__ long long lo(int c) const { return U * c / G; }
-  __host__ __device__ int cta_of(long long u) const { return (int)(((u + 1) * G - 1) / U); }
-  // Part of tile i that CTA c computes, as a slot of the workspace: a CTA has
-  // at most two parts, the one its run begins with and the one it ends with.
-  __host__ __device__ int slot(int c, long long i) const { return 2 * c + (lo(c) >= i * nk ? 0 : 1); }
+  int gran, x;             // a run is a multiple of gran units; W4X
+  int U, base, rem;        // units; CTA c's run: base * gran units, gran more for c < rem
+  __host__ __device__ int lo(int c) const { return (c * base + (c < rem ? c : rem)) * gran; }
+  // For gran = 1: the CTA of a unit, and the part of tile i that CTA c
+  // computes, as a slot of the workspace: a CTA has at most two parts, the one
+  // its run begins with and the one it ends with.
+  __host__ __device__ int cta_of(int u) const {
+    const int cut = rem * (base + 1);
+    return u < cut ? u / (base + 1) : rem + (u - cut) / base;
+  }
+  __host__ __device__ int slot(int c, int i) const { return 2 * c + (lo(c) >= i * nk ? 0 : 1); }
 };
 W4Work w4_work(const W4Params &p, int tn) {
   W4Work w;
+  const int NX = tn == 64 ? 4 : 8;
   w.nk = (p.K + kBlk - 1) / kBlk;
   w.nb = (p.N + kTileN - 1) / kTileN;
   w.ntt = (p.T + tn - 1) / tn;
-  w.U = (long long)p.groups * w.nb * w.ntt * w.nk;
-  w.G = (int)std::min<long long>(num_sms(), w.U);
+  const int tiles = p.groups * w.nb * w.ntt;
+  w.U = tiles * w.nk;
+  w.G = std::min(num_sms(), w.U);
+  w.gran = 1;
+  // whole tiles per CTA where the longest run gets at most 6 units longer by
+  // it: joining parts costs a launch, 2 to 3 us, and a unit about 0.4
+  const int wt = (tiles + num_sms() - 1) / num_sms();
+  if (wt * w.nk <= (w.U + w.G - 1) / w.G + 6) {
+    w.gran = w.nk;
+    w.G = (tiles + wt - 1) / wt;
+  }
+  w.base = w.U / w.gran / w.G;
+  w.rem = w.U / w.gran - w.base * w.G;
+  const int run = (w.base + (w.rem > 0)) * w.gran;   // the longest
+  w.x = w.ntt > 1 ? kRing : run <= NX ? kByUnit : p.groups == 1 && w.nk <= NX ? kByBlock : kRing;
   return w;
 }
+constexpr int kMaxT = 4096;               // tokens of one launch
 int w4_tn(const W4Params &p) { return p.T <= 16 ? 16 : p.T <= 32 ? 32 : 64; }
 
-// Workspace: x in f16, its factors, the parts.
+// Workspace: x in f16 and its factors (kRing), the parts of cut tiles.
 struct W4Ws {
   size_t x, d, part, bytes;
   int Kp;
@@ -116,11 +383,11 @@ W4Ws w4_ws(const W4Params &p) {
   const W4Work w = w4_work(p, tn);
   W4Ws l;
   l.Kp = w.nk * kBlk;
-  const size_t rows = (size_t)p.groups * p.T;
+  const size_t rows = w.x == kRing ? (size_t)p.groups * p.T : 0;
   l.x = 0;
   l.d = (rows * l.Kp * 2 + 255) & ~(size_t)255;
   l.part = l.d + ((rows * 4 + 255) & ~(size_t)255);
-  l.bytes = l.part + (size_t)2 * w.G * std::min(tn, p.T) * kTileN * 4;
+  l.bytes = l.part + (w.gran == 1 ? (size_t)2 * w.G * std::min(tn, p.T) * kTileN * 4 : 0);
   return l;
 }
 
@@ -138,11 +405,11 @@ struct W4Layout {
   // one ring of 4 stages for both, 54 with 7 of codes and 3 of x.
   static constexpr uint32_t kCodes = kTileN * 128, kX = 4 * TN * 128, kScales = 8 * 128;
   static constexpr uint32_t kStage = kCodes + kScales;
-  static constexpr int NC = TN == 64 ? 5 : TN == 32 ? 7 : 9, NX = TN == 64 ? 4 : TN == 32 ? 6 : 8;
+  static constexpr int NC = TN == 64 ? 5 : TN == 32 ? 5 : 9, NX = TN == 64 ? 4 : 8;
   static constexpr int ND = TN == 64 ? 1 : 2;
   static constexpr uint32_t kSecond = TN == 64 ? 64 : 32;   // column of the second accumulator in its pair
   static constexpr uint32_t x_off = NC * kStage;
-  static constexpr uint32_t bar_off = x_off + NX * kX;
+  static constexpr uint32_t xd_off = x_off + NX * kX, bar_off = xd_off + 512;
   static constexpr uint32_t bytes = bar_off + 512 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory");
 };
@@ -150,31 +417,83 @@ constexpr int kDecWarps = 16, kEpi0 = 2 + kDecWarps;     // first epilogue warp
 constexpr int kXWarp = kEpi0 + 4, kMma1 = kEpi0 + 5;    // x loads; MMAs of the second half (warp 1: of the first)
 constexpr int kW4Threads = (kMma1 + 1) * 32;
 
-// 32 codes of a 16-byte chunk as 16 f16 pairs, times the scale s2 (t2: INT4's offset).
-template <int CODE>
-__device__ __forceinline__ void w4_decode(const uint4 &q, uint32_t s2, uint32_t t2, uint32_t (&r)[16]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (CODE == HCA_W4_E2M1) {
-      uint32_t f[4];
-      e2m1x8_f16(w[i], f);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r[4 * i + j] = hmul2_u32(f[j], s2);
-    } else {
-      // u = code + 8 in 0..15 read as an e4m3 byte is u 2^-9 (subnormals, then exponent 1): the value
-      // (u - 8) 2^-9 s by one fused multiply-add, exact; the 2^9 is in the epilogue's factor
-      const uint32_t u = w[i] ^ 0x88888888u, a = u & 0x0F0F0F0Fu, d = (u >> 4) & 0x0F0F0F0Fu;
-      const uint32_t lo = __byte_perm(a, d, 0x5140), hi = __byte_perm(a, d, 0x7362);
-      r[4 * i] = hfma2_u32(e4m3x2_f16x2(lo), s2, t2);
-      r[4 * i + 1] = hfma2_u32(e4m3x2_f16x2(lo >> 16), s2, t2);
-      r[4 * i + 2] = hfma2_u32(e4m3x2_f16x2(hi), s2, t2);
-      r[4 * i + 3] = hfma2_u32(e4m3x2_f16x2(hi >> 16), s2, t2);
+// Barrier of the weight warps.
+__device__ __forceinline__ void w4_dec_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kDecWarps * 32) : "memory"); }
+
+// The weight warps' staging of x: `units` units of TN tokens as f16 in the
+// layout that the MMAs read, and the factor per token.  A warp takes a token
+// of a unit at a time, a lane 8 channels.  bf16 values whose token has its
+// largest in [1, 2^15) (among the units staged here) are stored as they are;
+// a token outside that range is stored again, scaled.
+template <int TN, typename XT>
+__device__ __forceinline__ void w4_stage_x(const W4Params &p, const W4Work &wk, int u0, int units, uint8_t *xs, float *xd,
+                                           uint32_t *amax) {
+  const int w = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, tid = threadIdx.x - 64;
+  // unit un of the run: channels from k of group g (a run may pass into further tiles and groups)
+  int first = 0, g0 = 0, t0 = 0;
+  if (wk.x == kByUnit) {
+    const int tile = u0 / wk.nk;
+    first = u0 - tile * wk.nk;
+    g0 = tile / wk.nb;
+    t0 = tile - g0 * wk.nb;
+  }
+  auto source = [&](int un, int row) -> const XT * {
+    int kb = first + un, g = g0, t = t0;
+    while (kb >= wk.nk) {
+      kb -= wk.nk;
+      if (++t == wk.nb) {
+        t = 0;
+        ++g;
+      }
     }
+    const int k = kb * kBlk + 8 * lane;
+    return row < p.T && k < p.K ? static_cast<const XT *>(p.x) + (long long)row * p.ldx + (long long)g * p.K + k : nullptr;
+  };
+  auto store = [&](int un, int row, const uint4 &h) {
+    *reinterpret_cast<uint4 *>(xs + un * W4Layout<TN>::kX + (lane / 8) * (TN * 128) + sw128_off(row, lane % 8)) = h;
+  };
+  if constexpr (sizeof(XT) == 1) {
+#pragma unroll 4
+    for (int c = w; c < units * TN; c += kDecWarps) {
+      const XT *x = source(c / TN, c % TN);
+      const uint2 u = x ? *reinterpret_cast<const uint2 *>(x) : make_uint2(0, 0);
+      store(c / TN, c % TN,
+            make_uint4(e4m3x2_f16x2(u.x), e4m3x2_f16x2(u.x >> 16), e4m3x2_f16x2(u.y), e4m3x2_f16x2(u.y >> 16)));
+    }
+    if (tid < p.T) xd[tid] = p.x_scale[tid];
+  } else {
+    if (tid < TN) amax[tid] = 0u;                  // |x| as bits, in the order of the values
+    w4_dec_sync();
+    auto f16 = [](const uint4 &u, float up) {
+      __half2 h[4] = {__floats2half2_rn(bf16_lo(u.x) * up, bf16_hi(u.x) * up), __floats2half2_rn(bf16_lo(u.y) * up, bf16_hi(u.y) * up),
+                      __floats2half2_rn(bf16_lo(u.z) * up, bf16_hi(u.z) * up), __floats2half2_rn(bf16_lo(u.w) * up, bf16_hi(u.w) * up)};
+      return *reinterpret_cast<const uint4 *>(h);
+    };
+#pragma unroll 4
+    for (int c = w; c < units * TN; c += kDecWarps) {
+      const XT *x = source(c / TN, c % TN);
+      const uint4 u = x ? *reinterpret_cast<const uint4 *>(x) : make_uint4(0, 0, 0, 0);
+      store(c / TN, c % TN, f16(u, 1.0f));
+      uint32_t am = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                             __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+      am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
+      if (lane == 0) atomicMax(&amax[c % TN], am);
+    }
+    w4_dec_sync();
+    // 2^e <= the largest value < 2^(e + 1), e at least -110 so that 2^(14 - e) and its inverse are normal
+    auto expo = [&](int row) { return max((int)(amax[row] >> 7) - 127, -110); };
+    auto kept = [&](int row) { return amax[row] == 0u || (expo(row) >= 0 && expo(row) < 15); };
+#pragma unroll 1
+    for (int c = w; c < units * TN; c += kDecWarps) {
+      if (kept(c % TN)) continue;
+      const XT *x = source(c / TN, c % TN);
+      store(c / TN, c % TN, f16(x ? *reinterpret_cast<const uint4 *>(x) : make_uint4(0, 0, 0, 0), pow2f(14 - expo(c % TN))));
+    }
+    if (tid < p.T) xd[tid] = kept(tid) ? 1.0f : pow2f(expo(tid) - 14);
   }
 }
 
-template <int TN, int CODE, typename OT>
+template <int TN, int CODE, typename XT, typename OT>
 __global__ void __launch_bounds__(kW4Threads, 1)
     w4_linear_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
                      const __grid_constant__ CUtensorMap tmX, W4Params p, W4Work wk, const float *xd, float *part) {
@@ -197,7 +516,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       mbar_init(bar(bars->c_empty[i]), kDecWarps);
     }
     for (int i = 0; i < L::NX; ++i) {
-      mbar_init(bar(bars->x_full[i]), 1);
+      mbar_init(bar(bars->x_full[i]), wk.x == kRing ? 1 : kDecWarps);
       mbar_init(bar(bars->x_empty[i]), 2);
     }
     for (int i = 0; i < 2 * kNA; ++i) {
@@ -218,22 +537,19 @@ __global__ void __launch_bounds__(kW4Threads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
-  const long long u0 = wk.lo(blockIdx.x), u1 = wk.lo(blockIdx.x + 1);
-  const int n = (int)(u1 - u0);
+  float *xds = reinterpret_cast<float *>(smem + L::xd_off);   // staged x: factors [64], maxima [64]
+  const int u0 = wk.lo(blockIdx.x), u1 = wk.lo(blockIdx.x + 1), n = u1 - u0;
   pdl_trigger();
 
   if (warp == 0 || warp == kXWarp) {
     if (lane == 0) {
-      // walks the units: the tile's place is worked out once per tile (64-bit
-      // divisions on every unit would cost the one issuing thread more than
-      // the unit's time)
-      long long tile = u0 / wk.nk;
-      int kb = (int)(u0 - tile * wk.nk), n0, g, row;
+      // walks the units; the tile's place is worked out once per tile
+      int tile = u0 / wk.nk, kb = u0 - tile * wk.nk, n0, g, row;
       auto place = [&]() {   // token tiles innermost: the CTAs of one weight block run together
-        const long long blk = tile / wk.ntt;
-        g = (int)(blk / wk.nb);
-        n0 = (int)(blk - (long long)g * wk.nb) * kTileN;
-        row = g * p.T + (int)(tile - blk * wk.ntt) * TN;
+        const int blk = tile / wk.ntt;
+        g = blk / wk.nb;
+        n0 = (blk - g * wk.nb) * kTileN;
+        row = g * p.T + (tile - blk * wk.ntt) * TN;
       };
       auto next = [&]() {
         if (++kb == wk.nk) {
@@ -257,7 +573,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
           tma_load_3d(a, &tmC, kb * (kBlk / 2), n0, g, b);
           tma_load_3d(a + L::kCodes, &tmS, n0, kb << sshift, g, b);
         }
-      } else {
+      } else if (wk.x == kRing) {
         tma_prefetch_desc(&tmX);
         pdl_wait();
         for (int i = 0; i < n; ++i, next()) {
@@ -275,7 +591,8 @@ __global__ void __launch_bounds__(kW4Threads, 1)
     constexpr uint32_t IDESC = idesc_f16(128, TN);
     const int half = warp == 1 ? 0 : 1;
     const uint64_t xdesc0 = sdesc_sw128(sbase + L::x_off, 16, 1024) + ((half * 2 * TN * 128) >> 4);
-    int ab = 0, xs = 0, left = wk.nk - (int)(u0 % wk.nk);   // left: units of the tile
+    int ab = 0, xs = 0, left = wk.nk - u0 % wk.nk;   // left: units of the tile
+    if (wk.x == kByBlock) xs = wk.nk - left;
     uint32_t aph = 0, xph = 0;
     bool ok = true;
     for (int i = 0, piece = 0; i < n && ok; ++piece) {
@@ -304,13 +621,23 @@ __global__ void __launch_bounds__(kW4Threads, 1)
           ab = 0;
           aph ^= 1;
         }
-        if (++xs == L::NX) {
+        // staged x stays in phase 0
+        if (++xs == (wk.x == kByBlock ? wk.nk : L::NX)) {
           xs = 0;
-          xph ^= 1;
+          xph ^= wk.x == kRing;
         }
       }
     }
   } else if (warp < kEpi0) {
+    if (wk.x != kRing) {
+      pdl_wait();   // x of the kernel before
+      const int units = wk.x == kByUnit ? n : wk.nk;
+      w4_stage_x<TN, XT>(p, wk, u0, units, smem + L::x_off, xds, reinterpret_cast<uint32_t *>(xds + 64));
+      fence_proxy_async();     // the tensor cores read it through the async proxy
+      __syncwarp();
+      if (lane == 0)
+        for (int i = 0; i < units; ++i) mbar_arrive(bar(bars->x_full[i]));
+    }
     // weights: row r of the tile, 16-byte chunks 2 kq and 2 kq + 1 of the stage's 8
     const int q = warp & 3, kq = (warp - 2) >> 2, r = q * 32 + lane;
     const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + kACol + kq * 32;
@@ -352,45 +679,53 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       }
     }
   } else {
-    // finished accumulators
-    pdl_wait();   // xd of the kernel before
+    // finished accumulators: thread = output row.  Short code, 8 tokens a step:
+    // a block runs it two or three times, so that fetching instructions is
+    // most of its cost (64 tokens unrolled by 16 with two 64-bit products per
+    // store: 9000 cycles per tile).
+    pdl_wait();   // xd of the kernel before; out may still be read by it
     const int q = warp & 3, f = q * 32 + lane;
     const uint32_t td = tmem + ((uint32_t)(q * 32) << 16);
+    bool ok = wk.x == kRing || mbar_wait_fast(bar(bars->x_full[0]), 0, p.status);   // xds is written
     int piece = 0;
-    for (long long u = u0; u < u1; ++piece) {
+    for (int u = u0; u < u1 && ok; ++piece) {
       const int d = piece % L::ND;
-      const long long tile = u / wk.nk, end = min((tile + 1) * wk.nk, u1);
+      const int tile = u / wk.nk, end = min((tile + 1) * wk.nk, u1);
       const bool whole = u == tile * wk.nk && end == (tile + 1) * wk.nk;
-      const uint32_t tp = td + d * 64;
-      const long long blk = tile / wk.ntt;
-      const int g = (int)(blk / wk.nb), o = (int)(blk - (long long)g * wk.nb) * kTileN + f;
-      const int t0 = (int)(tile - blk * wk.ntt) * TN, nt = min(TN, p.T - t0);
-      float rs = 0.f;
+      const int blk = tile / wk.ntt, g = blk / wk.nb, o = (blk - g * wk.nb) * kTileN + f;
+      const int t0 = (tile - blk * wk.ntt) * TN, nt = min(TN, p.T - t0);
+      if (wk.x == kRing) {
+        if (f < nt) xds[f] = xd[g * p.T + t0 + f];
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+      }
+      float rs = 1.f;
       if (whole && o < p.N) rs = p.row_scale[(long long)g * p.N + o] * (CODE == HCA_W4_INT4 ? 512.f : 1.f);
-      if (!mbar_wait_fast(bar(bars->d_full[d]), (piece / L::ND) & 1, p.status)) break;
-      tc_fence_after();
       float *pp = part + (long long)wk.slot(blockIdx.x, tile) * min(TN, p.T) * kTileN + f;
+      OT *po = static_cast<OT *>(p.out) + (long long)t0 * p.ldo + (long long)g * p.N + o;
+      ok = mbar_wait_fast(bar(bars->d_full[d]), (piece / L::ND) & 1, p.status);
+      if (!ok) break;
+      tc_fence_after();
 #pragma unroll 1
-      for (int j0 = 0; j0 < nt; j0 += 16) {
-        uint32_t v[16], v1[16];
-        tmem_ld_32x32b_x16(tp + j0, v);
-        tmem_ld_32x32b_x16(tp + L::kSecond + j0, v1);
+      for (int j0 = 0; j0 < nt; j0 += 8) {
+        uint32_t v[8], v1[8];
+        tmem_ld_32x32b_x8(td + d * 64 + j0, v);
+        tmem_ld_32x32b_x8(td + d * 64 + L::kSecond + j0, v1);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int t = j0 + j;
-          if (t < nt) {
-            const float a = __uint_as_float(v[j]) + __uint_as_float(v1[j]);
-            if (!whole) pp[t * kTileN] = a;
-            else if (o < p.N)
-              Elt<OT>::store(static_cast<OT *>(p.out) + (long long)(t0 + t) * p.ldo + (long long)g * p.N + o,
-                             a * rs * xd[g * p.T + t0 + t]);
+        for (int j = 0; j < 8; ++j) {
+          const float a = (__uint_as_float(v[j]) + __uint_as_float(v1[j])) * xds[j0 + j] * rs;
+          if (j0 + j < nt) {
+            if (!whole) *pp = a;
+            else if (o < p.N) Elt<OT>::store(po, a);
           }
+          pp += kTileN;
+          po += p.ldo;
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars->d_empty[d]));
+      if (wk.x == kRing) asm volatile("bar.sync 2, 128;" ::: "memory");   // xds has been read
       u = end;
     }
   }
@@ -403,16 +738,15 @@ __global__ void __launch_bounds__(kW4Threads, 1)
 // Tiles that were cut: their parts summed in the order of their channels.
 // Block = (tile, 4 tokens), thread = output.
 template <int TN, typename OT>
-__global__ void __launch_bounds__(kTileN) w4_join_kernel(W4Params p, W4Work wk, const float *xd, const float *part) {
-  const long long tile = blockIdx.x;
+__global__ void __launch_bounds__(kTileN) w4_join_kernel(W4Params p, W4Work wk, const float *part) {
+  const int tile = blockIdx.x;
   const int c0 = wk.cta_of(tile * wk.nk), c1 = wk.cta_of((tile + 1) * wk.nk - 1);
   if (c0 == c1) {
     pdl_wait();   // this grid may not end before the one that it depends on
     return;
   }
-  const long long blk = tile / wk.ntt;
-  const int g = (int)(blk / wk.nb), o = (int)(blk - (long long)g * wk.nb) * kTileN + threadIdx.x;
-  const int t0 = (int)(tile - blk * wk.ntt) * TN, tl = 4 * blockIdx.y, nt = min(4, min(TN, p.T - t0) - tl);
+  const int blk = tile / wk.ntt, g = blk / wk.nb, o = (blk - g * wk.nb) * kTileN + threadIdx.x;
+  const int t0 = (tile - blk * wk.ntt) * TN, tl = 4 * blockIdx.y, nt = min(4, min(TN, p.T - t0) - tl);
   const int per = min(TN, p.T) * kTileN;
   float rs = 0.f;
   if (o < p.N) rs = p.row_scale[(long long)g * p.N + o] * (p.code == HCA_W4_INT4 ? 512.f : 1.f);
@@ -430,12 +764,47 @@ __global__ void __launch_bounds__(kTileN) w4_join_kernel(W4Params p, W4Work wk, 
   for (int j = 0; j < 4; ++j)
     if (j < nt)
       Elt<OT>::store(static_cast<OT *>(p.out) + (long long)(t0 + tl + j) * p.ldo + (long long)g * p.N + o,
-                     acc[j] * rs * xd[g * p.T + t0 + tl + j]);
+                     acc[j] * rs);
+}
+
+// Up to 32 tokens whose x fits; the larger products of many tokens belong to
+// the tensor-memory kernel.
+bool w4_few(const W4Params &p) {
+  const int Kp = (p.K + 127) / 128 * 128, T8 = (p.T + 7) / 8 * 8;
+  return p.T <= 32 && (long long)T8 * Kp <= kFewElems && (long long)p.groups * p.N * p.K <= (4 << 20);
+}
+template <int MT, int NT, int CODE, typename XT, typename OT>
+int launch_few_t(const W4Params &p, cudaStream_t s) {
+  const int Kp = (p.K + 127) / 128 * 128;
+  // warps per row set: as many as keep the grid within two blocks per SM, at most one per 128 channels
+  int KS = kFewWarps;
+  auto blocks = [&](int ks) { return (p.N + 16 * MT * (kFewWarps / ks) - 1) / (16 * MT * (kFewWarps / ks)); };
+  while (KS > 1 && ((long long)blocks(KS) * p.groups > 2 * num_sms() || Kp / 128 < KS)) KS /= 2;
+  const size_t smem = std::max<size_t>((size_t)8 * NT * few_pitch(Kp), KS > 1 ? (size_t)kFewWarps * MT * NT * 512 : 0);
+  static std::atomic<bool> attr_dev[kMaxDevices];
+  std::atomic<bool> &attr = attr_dev[device_slot()];
+  if (!attr) {
+    const cudaError_t e = cudaFuncSetAttribute(w4_few_kernel<MT, NT, CODE, XT, OT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kFewElems * 2 + 32 * 32);
+    if (e != cudaSuccess) return fail(HCA_ERR_CUDA, "w4_linear smem attribute: %s", cudaGetErrorString(e));
+    attr = true;
+  }
+  return HCA_LAUNCH("w4_linear", s, w4_few_kernel<MT, NT, CODE, XT, OT><<<dim3(blocks(KS), p.groups), kFewWarps * 32, smem, s>>>(p, KS, Kp));
+}
+template <int CODE, typename XT, typename OT>
+int launch_few_c(const W4Params &p, cudaStream_t s) {
+  if (p.T <= 8) return launch_few_t<1, 1, CODE, XT, OT>(p, s);
+  if (p.T <= 16) return launch_few_t<2, 2, CODE, XT, OT>(p, s);
+  return launch_few_t<2, 4, CODE, XT, OT>(p, s);
+}
+template <typename XT, typename OT>
+int launch_few(const W4Params &p, cudaStream_t s) {
+  return p.code == HCA_W4_E2M1 ? launch_few_c<HCA_W4_E2M1, XT, OT>(p, s) : launch_few_c<HCA_W4_INT4, XT, OT>(p, s);
 }
 
 template <typename... KArgs, typename... Args>
-int w4_launch(const char *name, dim3 grid, int threads, size_t smem, cudaStream_t s, void (*kernel)(KArgs...),
-              Args... args) {
+int w4_launch(const char *name, dim3 grid, int threads, size_t smem, cudaStream_t s, bool dependent,
+              void (*kernel)(KArgs...), Args... args) {
   LaunchScope ls(name, s);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
@@ -446,7 +815,7 @@ int w4_launch(const char *name, dim3 grid, int threads, size_t smem, cudaStream_
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = dependent ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
@@ -455,13 +824,13 @@ int w4_launch(const char *name, dim3 grid, int threads, size_t smem, cudaStream_
   return ls.done();
 }
 
-template <int TN, int CODE, typename OT>
+template <int TN, int CODE, typename XT, typename OT>
 int launch_w4_t(const W4Params &p, cudaStream_t s) {
   using L = W4Layout<TN>;
   static std::atomic<bool> attr_dev[kMaxDevices];
   std::atomic<bool> &attr = attr_dev[device_slot()];
   if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(w4_linear_kernel<TN, CODE, OT>,
+    const cudaError_t e = cudaFuncSetAttribute(w4_linear_kernel<TN, CODE, XT, OT>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::bytes);
     if (e != cudaSuccess) return fail(HCA_ERR_CUDA, "w4_linear smem attribute: %s", cudaGetErrorString(e));
     attr = true;
@@ -470,6 +839,7 @@ int launch_w4_t(const W4Params &p, cudaStream_t s) {
   const W4Ws l = w4_ws(p);
   char *ws = static_cast<char *>(p.ws);
   float *xd = reinterpret_cast<float *>(ws + l.d), *part = reinterpret_cast<float *>(ws + l.part);
+  __half *xh = reinterpret_cast<__half *>(ws + l.x);
   CUtensorMap tmC, tmS, tmX;
   int rc = encode_tmap_3d(&tmC, p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)p.K / 2, (uint64_t)p.N,
                           (uint64_t)p.groups, (uint64_t)p.K / 2, (uint64_t)p.N * (p.K / 2), 128, kTileN,
@@ -478,23 +848,34 @@ int launch_w4_t(const W4Params &p, cudaStream_t s) {
     rc = encode_tmap_3d(&tmS, p.scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)p.ldn, (uint64_t)(p.K / p.G),
                         (uint64_t)p.groups, (uint64_t)p.ldn, (uint64_t)p.ldn * (p.K / p.G), kTileN, kBlk / p.G,
                         CU_TENSOR_MAP_SWIZZLE_NONE);
-  if (!rc)
-    rc = encode_tmap_2d(&tmX, ws + l.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)l.Kp, (uint64_t)p.groups * p.T,
+  if (!rc && wk.x == kRing)
+    rc = encode_tmap_2d(&tmX, xh, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)l.Kp, (uint64_t)p.groups * p.T,
                         (uint64_t)l.Kp * 2, 64, TN, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc) return rc;
-  rc = w4_launch("w4_linear", dim3(wk.G), kW4Threads, L::bytes, s, w4_linear_kernel<TN, CODE, OT>, tmC, tmS, tmX, p, wk,
-                 (const float *)xd, part);
-  if (rc || wk.U % wk.G == 0 && (wk.U / wk.G) % wk.nk == 0) return rc;   // every run is made of whole tiles
-  return w4_launch("w4_join", dim3((unsigned)(wk.U / wk.nk), (std::min(TN, p.T) + 3) / 4), kTileN, 0, s,
-                   w4_join_kernel<TN, OT>, p, wk, (const float *)xd, (const float *)part);
+  if (wk.x == kRing) {
+    rc = HCA_LAUNCH("w4_x", s, w4_x_kernel<XT><<<(unsigned)p.groups * p.T, 256, 0, s>>>(p, xh, xd, l.Kp));
+    if (rc) return rc;
+  } else {
+    tmX = tmC;      // not used
+  }
+  // dependent on w4_x only; without it an ordinary launch, since the weights are read before any wait
+  rc = w4_launch("w4_linear", dim3(wk.G), kW4Threads, L::bytes, s, wk.x == kRing, w4_linear_kernel<TN, CODE, XT, OT>,
+                 tmC, tmS, tmX, p, wk, (const float *)xd, part);
+  if (rc || wk.gran > 1) return rc;
+  return w4_launch("w4_join", dim3((unsigned)(wk.U / wk.nk), (std::min(TN, p.T) + 3) / 4), kTileN, 0, s, true,
+                   w4_join_kernel<TN, OT>, p, wk, (const float *)part);
 }
 template <int TN, int CODE>
-int launch_w4_o(const W4Params &p, hca_dtype od, cudaStream_t s) {
-  return od == HCA_F32 ? launch_w4_t<TN, CODE, float>(p, s) : launch_w4_t<TN, CODE, __nv_bfloat16>(p, s);
+int launch_w4_o(const W4Params &p, hca_dtype xd, hca_dtype od, cudaStream_t s) {
+  if (xd == HCA_BF16)
+    return od == HCA_F32 ? launch_w4_t<TN, CODE, __nv_bfloat16, float>(p, s)
+                         : launch_w4_t<TN, CODE, __nv_bfloat16, __nv_bfloat16>(p, s);
+  return od == HCA_F32 ? launch_w4_t<TN, CODE, unsigned char, float>(p, s)
+                       : launch_w4_t<TN, CODE, unsigned char, __nv_bfloat16>(p, s);
 }
 template <int TN>
-int launch_w4_c(const W4Params &p, hca_dtype od, cudaStream_t s) {
-  return p.code == HCA_W4_E2M1 ? launch_w4_o<TN, HCA_W4_E2M1>(p, od, s) : launch_w4_o<TN, HCA_W4_INT4>(p, od, s);
+int launch_w4_c(const W4Params &p, hca_dtype xd, hca_dtype od, cudaStream_t s) {
+  return p.code == HCA_W4_E2M1 ? launch_w4_o<TN, HCA_W4_E2M1>(p, xd, od, s) : launch_w4_o<TN, HCA_W4_INT4>(p, xd, od, s);
 }
 
 __device__ __forceinline__ float load_w(const float *p) { return *p; }
@@ -542,22 +923,34 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const T *__restrict__ 
 
 }  // namespace
 
-size_t w4_workspace_bytes(const W4Params &p) { return p.T > 0 ? w4_ws(p).bytes : 0; }
+size_t w4_workspace_bytes(const W4Params &p) {
+  if (p.T <= 0 || w4_few(p)) return 0;
+  W4Params c = p;
+  c.T = std::min(p.T, kMaxT);
+  const size_t most = w4_ws(c).bytes;
+  c.T = p.T % kMaxT;                        // a last, shorter run may be laid out otherwise
+  return c.T && p.T > kMaxT ? std::max(most, w4_ws(c).bytes) : most;
+}
 
 int launch_w4_linear(const W4Params &p, hca_dtype xd, hca_dtype od, cudaStream_t s) {
   if (p.T == 0) return HCA_OK;
-  const W4Ws l = w4_ws(p);
-  char *ws = static_cast<char *>(p.ws);
-  __half *xh = reinterpret_cast<__half *>(ws + l.x);
-  float *f = reinterpret_cast<float *>(ws + l.d);
-  const unsigned rows = (unsigned)p.groups * p.T;
-  const int rc =
-      xd == HCA_BF16
-          ? HCA_LAUNCH("w4_x", s, w4_x_kernel<__nv_bfloat16><<<rows, 256, 0, s>>>(p, xh, f, l.Kp))
-          : HCA_LAUNCH("w4_x", s, w4_x_kernel<unsigned char><<<rows, 256, 0, s>>>(p, xh, f, l.Kp));
-  if (rc) return rc;
-  const int tn = w4_tn(p);
-  return tn == 16 ? launch_w4_c<16>(p, od, s) : tn == 32 ? launch_w4_c<32>(p, od, s) : launch_w4_c<64>(p, od, s);
+  if (w4_few(p)) {
+    if (xd == HCA_BF16) return od == HCA_F32 ? launch_few<__nv_bfloat16, float>(p, s) : launch_few<__nv_bfloat16, __nv_bfloat16>(p, s);
+    return od == HCA_F32 ? launch_few<unsigned char, float>(p, s) : launch_few<unsigned char, __nv_bfloat16>(p, s);
+  }
+  // many tokens: runs of at most kMaxT, so that unit numbers stay within 31 bits
+  W4Params c = p;
+  for (int t0 = 0; t0 < p.T; t0 += kMaxT) {
+    c.T = std::min(kMaxT, p.T - t0);
+    c.x = static_cast<const char *>(p.x) + (long long)t0 * p.ldx * (xd == HCA_BF16 ? 2 : 1);
+    if (p.x_scale) c.x_scale = p.x_scale + t0;
+    c.out = static_cast<char *>(p.out) + (long long)t0 * p.ldo * (od == HCA_BF16 ? 2 : 4);
+    const int tn = w4_tn(c);
+    const int rc = tn == 16 ? launch_w4_c<16>(c, xd, od, s)
+                   : tn == 32 ? launch_w4_c<32>(c, xd, od, s) : launch_w4_c<64>(c, xd, od, s);
+    if (rc) return rc;
+  }
+  return HCA_OK;
 }
 
 int launch_w4_quantize(const void *w, hca_dtype wd, const W4Params &p, void *codes, void *scales, float *row_scale,

@@ -11,7 +11,7 @@ from long_context_compressed_hca_b200 import build as hbuild
 from tests import lowbit_reference as R
 
 X = 1 << 20          # made-up device addresses, never read: every call here is refused or empty
-P = [X * (i + 1) for i in range(9)]
+P = [16 * X * (i + 1) for i in range(9)]
 
 
 @pytest.fixture(scope="module")
@@ -75,12 +75,13 @@ def test_w4_refusals(L):
     _bad(call(x_dtype=hb.HCA_FP8E4M3), "x_scale")
     _bad(call(o=P[4] + 4), "aligned")
     _bad(call(o=P[0]), "out overlaps")
-    d = hb.w4_desc(4, 64, 256)
-    need = L.hca_w4_linear_workspace_size(d)
-    if need:
-        _bad(call(nws=need - 1), "workspace too small")
-        _bad(call(ws=None), "workspace too small")
-        _bad(call(ws=P[1]), "workspace overlaps")
+    big = dict(T=64, N=256, K=8192)
+    need = L.hca_w4_linear_workspace_size(hb.w4_desc(**big))
+    assert 0 < need <= 1 << 22
+    _bad(call(nws=need - 1, **big), "workspace too small")
+    _bad(call(ws=None, nws=1 << 30, **big), "workspace too small")
+    _bad(call(ws=P[1], nws=need, **big), "workspace overlaps")
+    _bad(call(o=P[5] + 256, nws=need, **big), "out overlaps")
     assert L.hca_w4_linear_workspace_size(hb.w4_desc(4, 64, 48)) == 0
     assert call(T=0, x=None, c=None, s=None, r=None, o=None, ws=None, nws=0) == hb.HCA_OK
     d = hb.w4_desc(0, 64, 256)
