@@ -191,7 +191,8 @@ def ptr(t):
 
 def stream_handle(stream=None):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: building a Stream object costs more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -466,27 +467,33 @@ _CODE_TYPES = {HCA_F32: (torch.float32,), HCA_BF16: (torch.bfloat16,),
 _F32, _BF16, _U8, _I32, _I64 = ((t,) for t in (torch.float32, torch.bfloat16, torch.uint8, torch.int32, torch.int64))
 
 
-def _tensor(name, t, shape, types, ld=None):
-    """t on the current device, of one of the types and the shape; dense, or with rows ld elements apart."""
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+def _tensor(name, t, shape, types, dev, ld=0):
+    """Address of t, which is on device dev, of one of the types and the shape; dense, or with rows ld elements apart."""
+    if t.get_device() == dev and t.dtype in types and t.shape == shape and (
+            t.is_contiguous() if not ld else
+            (shape[1] == 1 or t.stride(1) == 1) and (shape[0] <= 1 or t.stride(0) == ld)):
+        return t.data_ptr()
+    if t.get_device() != dev:
         _bad(f"{name} must be on the current CUDA device (it is on {t.device})")
     if t.dtype not in types:
         _bad(f"{name} has dtype {t.dtype}, expected {types[0] if types else 'another'}")
     if t.shape != shape:
         _bad(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if ld is None or ld == shape[1]:
-        if not t.is_contiguous():
-            _bad(f"{name} must be contiguous")
-    elif (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) != ld):
-        _bad(f"{name} must have contiguous rows {ld} elements apart")
-    return t.data_ptr()
+    _bad(f"{name} must have contiguous rows {ld} elements apart" if ld else f"{name} must be contiguous")
 
 
-def _scratch(ws):
+def _device(t):
+    """The current device, which has to be the one of t."""
+    if not t.is_cuda:
+        _bad("tensors must be on the current CUDA device (one is on the host)")
+    return torch.cuda.current_device()
+
+
+def _scratch(ws, dev):
     """(address, bytes) of a workspace tensor, or of none."""
     if ws is None:
         return None, 0
-    return _tensor("ws", ws, ws.shape, (ws.dtype,)), ws.numel() * ws.element_size()
+    return _tensor("ws", ws, ws.shape, (ws.dtype,), dev), ws.numel() * ws.element_size()
 
 
 def norm_desc(rows, d, x_dtype=HCA_BF16, res_dtype=None, out_dtype=HCA_BF16, scale_group=0, eps=1e-6, ldx=0, ldr=0,
@@ -497,18 +504,19 @@ def norm_desc(rows, d, x_dtype=HCA_BF16, res_dtype=None, out_dtype=HCA_BF16, sca
 
 def add_rms_norm(d: NormDesc, x, res, gamma, res_out, out, out_scale=None, stream=None):
     """out = RMSNorm(x + res) * gamma (e4m3 with out_scale, or bf16 / f32), res_out = x + res; see hca_add_rms_norm."""
-    shape = (d.rows, d.d)
-    px = _tensor("x", x, shape, _CODE_TYPES.get(d.x_dtype, ()), d.ldx or d.d)
-    rt = _CODE_TYPES.get(d.res_dtype, ())
-    pr = None if res is None else _tensor("res", res, shape, rt, d.ldr or d.d)
-    pro = None if res_out is None else _tensor("res_out", res_out, shape, rt, d.ldr or d.d)
-    pg = None if gamma is None else _tensor("gamma", gamma, (d.d,), _F32)
-    po = _tensor("out", out, shape, _CODE_TYPES.get(d.out_dtype, ()), d.ldo or d.d)
+    dev, width, od = _device(x), d.d, d.out_dtype
+    shape, rt, ldr = (d.rows, width), _CODE_TYPES.get(d.res_dtype, ()), d.ldr
+    px = _tensor("x", x, shape, _CODE_TYPES.get(d.x_dtype, ()), dev, d.ldx)
+    pr = None if res is None else _tensor("res", res, shape, rt, dev, ldr)
+    pro = None if res_out is None else _tensor("res_out", res_out, shape, rt, dev, ldr)
+    pg = None if gamma is None else _tensor("gamma", gamma, (width,), _F32, dev)
+    po = _tensor("out", out, shape, _CODE_TYPES.get(od, ()), dev, d.ldo)
     ps = None
-    if d.out_dtype == HCA_FP8E4M3:
+    if od == HCA_FP8E4M3:
         if out_scale is None:
             _bad("an e4m3 output needs out_scale")
-        ps = _tensor("out_scale", out_scale, (d.rows, d.d // d.scale_group if d.scale_group > 0 else 1), _F32)
+        group = d.scale_group
+        ps = _tensor("out_scale", out_scale, (shape[0], width // group if group > 0 else 1), _F32, dev)
     return check(lib().hca_add_rms_norm(d, px, pr, pg, pro, po, ps, stream_handle(stream)))
 
 
@@ -523,24 +531,24 @@ def w4_linear_workspace_size(d: W4Desc) -> int:
 
 def w4_linear(d: W4Desc, x, x_scale, codes, scales, row_scale, out, ws, stream=None):
     """out = x @ W^T for 4-bit weights (w4_quantize) and T tokens; see hca_w4_linear."""
-    px = _tensor("x", x, (d.T, d.groups * d.K), _CODE_TYPES.get(d.x_dtype, ()), d.ldx or d.groups * d.K)
+    dev, T, N, K, groups = _device(x), d.T, d.N, d.K, d.groups
+    px = _tensor("x", x, (T, groups * K), _CODE_TYPES.get(d.x_dtype, ()), dev, d.ldx)
     ps = None
     if x_scale is not None:
         if x_scale.dim() == 2:          # one scale per row as add_rms_norm writes them
             x_scale = x_scale.view(-1)
-        ps = _tensor("x_scale", x_scale, (d.T,), _F32)
-    pc = _tensor("codes", codes, (d.groups * d.N, d.K // 2), _U8)
-    pw = _tensor("scales", scales, (d.groups, d.K // max(d.scale_group, 1), (d.N + 15) // 16 * 16),
-                 _CODE_TYPES[HCA_FP8E4M3])
-    pr = _tensor("row_scale", row_scale, (d.groups * d.N,), _F32)
-    po = _tensor("out", out, (d.T, d.groups * d.N), _CODE_TYPES.get(d.out_dtype, ()), d.ldo or d.groups * d.N)
-    pws, nws = _scratch(ws)
+        ps = _tensor("x_scale", x_scale, (T,), _F32, dev)
+    pc = _tensor("codes", codes, (groups * N, K // 2), _U8, dev)
+    pw = _tensor("scales", scales, (groups, K // max(d.scale_group, 1), (N + 15) // 16 * 16), _CODE_TYPES[HCA_FP8E4M3], dev)
+    pr = _tensor("row_scale", row_scale, (groups * N,), _F32, dev)
+    po = _tensor("out", out, (T, groups * N), _CODE_TYPES.get(d.out_dtype, ()), dev, d.ldo)
+    pws, nws = _scratch(ws, dev)
     return check(lib().hca_w4_linear(d, px, ps, pc, pw, pr, po, pws, nws, stream_handle(stream)))
 
 
 def w4_quantize(d: W4Desc, w, stream=None):
     """(codes, scales, row_scale) of weights w [groups*N, K], as w4_linear takes them."""
-    pw = _tensor("w", w, (d.groups * d.N, d.K), (torch.float32, torch.bfloat16))
+    pw = _tensor("w", w, (d.groups * d.N, d.K), (torch.float32, torch.bfloat16), _device(w))
     codes = torch.empty(d.groups * d.N, d.K // 2, dtype=torch.uint8, device=w.device)
     scales = torch.empty(d.groups, d.K // max(d.scale_group, 1), (d.N + 15) // 16 * 16, dtype=torch.uint8,
                          device=w.device)
@@ -555,28 +563,28 @@ def kv_fp4_row_bytes(c, rd) -> int:
     return lib().hca_kv_fp4_row_bytes(c, rd)
 
 
-def _fp4_records(name, t, c, rd):
+def _fp4_records(name, t, c, rd, dev):
     rec = lib().hca_kv_fp4_row_bytes(c, rd)
     if rec == 0:
         _bad(f"unsupported (c, rd) = ({c}, {rd})")
-    return _tensor(name, t, t.shape[:-1] + (rec,), _U8), t.numel() // rec
+    return _tensor(name, t, t.shape[:-1] + (rec,), _U8, dev), t.numel() // rec
 
 
 def kv_quant_fp4(x, c, rd, records, slots=None, stream=None):
     """Rows x [rows, c] to 4-bit records: row r to record slots[r] (int64; r without slots)."""
-    po, n = _fp4_records("records", records, c, rd)
-    rows = x.shape[0]
-    px = _tensor("x", x, (rows, c), (torch.bfloat16, torch.float32))
-    ps = None if slots is None else _tensor("slots", slots, (rows,), _I64)
+    dev, rows = _device(x), x.shape[0]
+    po, n = _fp4_records("records", records, c, rd, dev)
+    px = _tensor("x", x, (rows, c), (torch.bfloat16, torch.float32), dev)
+    ps = None if slots is None else _tensor("slots", slots, (rows,), _I64, dev)
     return check(lib().hca_kv_quant_fp4(px, DTYPE_CODE[x.dtype], rows, c, rd, po, n, ps, stream_handle(stream)))
 
 
 def kv_dequant_fp4(records, c, rd, out, slots=None, stream=None):
     """4-bit records slots[r] (record r without slots) as bf16 rows out [rows, c]."""
-    pi, n = _fp4_records("records", records, c, rd)
-    rows = out.shape[0]
-    po = _tensor("out", out, (rows, c), _BF16)
-    ps = None if slots is None else _tensor("slots", slots, (rows,), _I64)
+    dev, rows = _device(out), out.shape[0]
+    pi, n = _fp4_records("records", records, c, rd, dev)
+    po = _tensor("out", out, (rows, c), _BF16, dev)
+    ps = None if slots is None else _tensor("slots", slots, (rows,), _I64, dev)
     return check(lib().hca_kv_dequant_fp4(pi, n, ps, rows, c, rd, po, stream_handle(stream)))
 
 
@@ -603,17 +611,19 @@ def attend_fp4_workspace_size(d: AttnDesc, max_pos) -> int:
 
 def attend_fp4(d: AttnDesc, q, cache: Fp4CacheHandle, idx, kv_win, sink, positions, max_pos, o, ws, stream=None):
     """Decode attention over a cache of 4-bit records, one position per sequence; see hca_attend_fp4."""
-    pq = _tensor("q", q, (d.B, d.n_h, d.c), _BF16)
-    po = _tensor("o", o, (d.B, d.n_h, d.c), _BF16)
-    _fp4_records("cache rows", cache.rows, d.c, d.rd)
+    dev, B, c = _device(q), d.B, d.c
+    shape = (B, d.n_h, c)
+    pq = _tensor("q", q, shape, _BF16, dev)
+    po = _tensor("o", o, shape, _BF16, dev)
+    _fp4_records("cache rows", cache.rows, c, d.rd, dev)
     if cache.pages is not None:
-        _tensor("pages", cache.pages, (d.B, cache.pages.shape[1]), _I32)
-    elif cache.rows.shape[0] != d.B:
-        _bad(f"the cache has {cache.rows.shape[0]} sequences, expected {d.B}")
-    pi = None if idx is None else _tensor("idx", idx, (d.B, d.k), _I32)
-    pk = None if kv_win is None else _tensor("kv_win", kv_win, (d.B, max(d.w, 1), d.c), _BF16)
-    ps = None if sink is None else _tensor("sink", sink, (d.n_h,), _F32)
-    pp = _tensor("positions", positions, (d.B,), _I32)
-    pws, nws = _scratch(ws)
+        _tensor("pages", cache.pages, (B, cache.pages.shape[1]), _I32, dev)
+    elif cache.rows.shape[0] != B:
+        _bad(f"the cache has {cache.rows.shape[0]} sequences, expected {B}")
+    pi = None if idx is None else _tensor("idx", idx, (B, d.k), _I32, dev)
+    pk = None if kv_win is None else _tensor("kv_win", kv_win, (B, max(d.w, 1), c), _BF16, dev)
+    ps = None if sink is None else _tensor("sink", sink, (d.n_h,), _F32, dev)
+    pp = _tensor("positions", positions, (B,), _I32, dev)
+    pws, nws = _scratch(ws, dev)
     return check(lib().hca_attend_fp4(d, pq, cache.struct, pi, pk, ps, pp, max_pos, po, pws, nws,
                                       stream_handle(stream)))

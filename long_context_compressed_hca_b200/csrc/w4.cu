@@ -22,8 +22,22 @@ constexpr int kBlk = 256;        // channels of one work unit (one pipeline stag
 constexpr int kTileN = 128;      // outputs of one tile: the MMA's M
 
 // ---------------------------------------------------------------- codes
-// Eight codes as f16 pairs in the order of their channels, times the scale s2
-// (INT4: t2 = -8 units of it).
+// Eight codes as f16 pairs, times the scale s2 (INT4: plus t2).  E2M1 pairs
+// are neighbouring channels.  INT4 pairs are channels (i, i + 4), which the
+// masks leave in place, and x is laid out alike (pair4): u = code + 8 under
+// the exponent of 1024 is the f16 value 1024 + u, and (1024 + u) s - 1032 s by
+// one fused multiply-add is (u - 8) s, exact since 1032 s has at most 11
+// significant bits.  s is the scale times 2^-9 there so that 1032 s stays in
+// range; the 2^9 is in the epilogue's factor.
+template <int CODE>
+__device__ __forceinline__ void w4_scale(uint32_t byte, uint32_t &s2, uint32_t &t2) {
+  s2 = e4m3_f16x2_dup(byte);
+  t2 = 0u;
+  if constexpr (CODE == HCA_W4_INT4) {
+    s2 = hmul2_u32(s2, 0x18001800u);        // 2^-9
+    t2 = hmul2_u32(s2, 0xE408E408u);        // -1032
+  }
+}
 template <int CODE>
 __device__ __forceinline__ void w4_decode8(uint32_t w, uint32_t s2, uint32_t t2, uint32_t *r) {
   if constexpr (CODE == HCA_W4_E2M1) {
@@ -32,15 +46,26 @@ __device__ __forceinline__ void w4_decode8(uint32_t w, uint32_t s2, uint32_t t2,
 #pragma unroll
     for (int j = 0; j < 4; ++j) r[j] = hmul2_u32(f[j], s2);
   } else {
-    // u = code + 8 in 0..15 read as an e4m3 byte is u 2^-9 (subnormals, then exponent 1): the value
-    // (u - 8) 2^-9 s by one fused multiply-add, exact; the 2^9 is in the epilogue's factor
-    const uint32_t u = w ^ 0x88888888u, a = u & 0x0F0F0F0Fu, d = (u >> 4) & 0x0F0F0F0Fu;
-    const uint32_t lo = __byte_perm(a, d, 0x5140), hi = __byte_perm(a, d, 0x7362);
-    r[0] = hfma2_u32(e4m3x2_f16x2(lo), s2, t2);
-    r[1] = hfma2_u32(e4m3x2_f16x2(lo >> 16), s2, t2);
-    r[2] = hfma2_u32(e4m3x2_f16x2(hi), s2, t2);
-    r[3] = hfma2_u32(e4m3x2_f16x2(hi >> 16), s2, t2);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = hfma2_u32(((w >> (4 * j)) & 0x000F000Fu) ^ 0x64086408u, s2, t2);
   }
+}
+// Eight values of x in the order of the pairs.
+template <int CODE>
+__device__ __forceinline__ uint4 w4_x8(const float (&v)[8]) {
+  __half2 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = CODE == HCA_W4_INT4 ? __floats2half2_rn(v[i], v[i + 4]) : __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+  return *reinterpret_cast<const uint4 *>(h);
+}
+template <int CODE>
+__device__ __forceinline__ uint4 w4_x8(const uint2 &u) {   // e4m3
+  if constexpr (CODE == HCA_W4_INT4)
+    return make_uint4(e4m3x2_f16x2(__byte_perm(u.x, u.y, 0x40)), e4m3x2_f16x2(__byte_perm(u.x, u.y, 0x51)),
+                      e4m3x2_f16x2(__byte_perm(u.x, u.y, 0x62)), e4m3x2_f16x2(__byte_perm(u.x, u.y, 0x73)));
+  else
+    return make_uint4(e4m3x2_f16x2(u.x), e4m3x2_f16x2(u.x >> 16), e4m3x2_f16x2(u.y), e4m3x2_f16x2(u.y >> 16));
 }
 // The 32 of a 16-byte chunk.
 template <int CODE>
@@ -54,25 +79,16 @@ __device__ __forceinline__ void w4_decode(const uint4 &q, uint32_t s2, uint32_t 
 // ---------------------------------------------------------------- x in f16
 // Row (g, t) of the workspace: K f16 values, zeros up to Kp, and the factor
 // that the sum over them is multiplied by.
-template <typename XT>
+template <int CODE, typename XT>
 __global__ void __launch_bounds__(256) w4_x_kernel(W4Params p, __half *xh, float *xd, int Kp) {
   __shared__ float part[8];
   pdl_trigger();   // the product kernel may start on its weights
   const int r = blockIdx.x, g = r / p.T, t = r - g * p.T, tid = threadIdx.x;
   const XT *x = static_cast<const XT *>(p.x) + (long long)t * p.ldx + (long long)g * p.K;
-  __half *o = xh + (long long)r * Kp;
+  uint4 *o = reinterpret_cast<uint4 *>(xh + (long long)r * Kp);
   if constexpr (sizeof(XT) == 1) {
-    for (int k = 16 * tid; k < Kp; k += 16 * 256) {
-      uint32_t h[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-      if (k < p.K) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(x + k);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = e4m3x2_f16x2(w[i >> 1] >> (16 * (i & 1)));
-      }
-      reinterpret_cast<uint4 *>(o + k)[0] = make_uint4(h[0], h[1], h[2], h[3]);
-      reinterpret_cast<uint4 *>(o + k)[1] = make_uint4(h[4], h[5], h[6], h[7]);
-    }
+    for (int k = tid; k < Kp / 8; k += 256)
+      o[k] = w4_x8<CODE>(8 * k < p.K ? reinterpret_cast<const uint2 *>(x)[k] : make_uint2(0, 0));
     if (tid == 0) xd[r] = p.x_scale[t];
   } else {
     float am = 0.f;
@@ -91,225 +107,15 @@ __global__ void __launch_bounds__(256) w4_x_kernel(W4Params p, __half *xh, float
     // e: am = f * 2^e, 1 <= f < 2, not below -110 so that 2^(14 - e) and its inverse are normal
     const int e = max((int)((__float_as_uint(am) >> 23) & 0xFFu) - 127, -110);
     const float up = pow2f(14 - e);
-    for (int k = 8 * tid; k < Kp; k += 8 * 256) {
+    for (int k = tid; k < Kp / 8; k += 256) {
       float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (k < p.K) load8(x + k, v);
-      __half2 h[4];
+      if (8 * k < p.K) load8(x + 8 * k, v);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i] * up, v[2 * i + 1] * up);
-      *reinterpret_cast<uint4 *>(o + k) = *reinterpret_cast<const uint4 *>(h);
+      for (int i = 0; i < 8; ++i) v[i] *= up;
+      o[k] = w4_x8<CODE>(v);
     }
     if (tid == 0) xd[r] = pow2f(e - 14);
   }
-}
-
-// ---------------------------------------------------------------- few tokens
-// One launch and no workspace when x of all tokens fits in shared memory: a
-// block stages it as f16 (scaled as above; the block holds whole rows, so it
-// finds their maxima itself) and its 8 warps multiply 16 MT weight rows each
-// by mma.sync with the decoded codes as the A fragment, read from global
-// memory where they are needed.  The order of the channels inside an MMA is
-// free as long as A and B agree: lane t of a quad holds 32 successive ones of
-// 128, 16 bytes of codes.  With few rows KS warps share them, each with a part
-// of the channels, and are added in a fixed order.
-// Against the kernel below (its three launches and pipeline fill): 1 x 512 x
-// 4096 12.1 us -> see kFewElems.
-constexpr int kFewWarps = 8;
-constexpr int kFewElems = 96 * 1024;    // staged values: 192 KB
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Staged row pitch in bytes: 128-byte multiples plus 32, so that the 16-byte
-// reads of 2 tokens x 4 quad lanes fall into different banks.
-__host__ __device__ constexpr int few_pitch(int Kp) { return Kp * 2 + 32; }
-
-template <int MT, int NT, int CODE, typename XT, typename OT>
-__global__ void __launch_bounds__(kFewWarps * 32, 2) w4_few_kernel(W4Params p, int KS, int Kp) {
-  extern __shared__ __align__(16) uint8_t sm[];
-  __shared__ float xd[8 * NT];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.y;
-  const int t = lane & 3, gr = lane >> 2;
-  const int ks = warp % KS, rb = warp / KS;
-  const int row0 = (blockIdx.x * (kFewWarps / KS) + rb) * 16 * MT;
-  const int nblk = Kp / 128, b0 = (int)((long long)ks * nblk / KS), b1 = (int)((long long)(ks + 1) * nblk / KS);
-  const int pitch = few_pitch(Kp);
-
-  // this lane's 16 bytes of block b for row `row0 + 16 m + gr + 8 h`
-  const int nrow[2] = {row0 + gr, row0 + gr + 8};
-  auto load = [&](int b, uint4 (&v)[MT][2], uint32_t (&sc)[MT][2]) {
-    const int k = b * 128 + 32 * t;
-    const bool in = k < p.K;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = nrow[h] + 16 * m;
-        const bool on = in && r < p.N;
-        v[m][h] = on ? __ldg(reinterpret_cast<const uint4 *>(p.codes + ((long long)g * p.N + r) * (p.K / 2) + k / 2))
-                     : make_uint4(0, 0, 0, 0);
-        sc[m][h] = on ? __ldg(p.scales + ((long long)g * (p.K / p.G) + k / p.G) * p.ldn + r) : 0u;
-      }
-  };
-  // PF blocks of codes are on their way at a time, the first of them while x is staged
-  constexpr int PF = MT == 1 ? 4 : 2;
-  uint4 v[PF][MT][2];
-  uint32_t sc[PF][MT][2];
-#pragma unroll
-  for (int u = 0; u < PF; ++u)
-    if (b0 + u < b1) load(b0 + u, v[u], sc[u]);
-
-  // ---- x of all tokens as f16; rows of tokens beyond the last are zero
-  const int per = Kp / 8, tot = p.T * per;               // 8-value chunks, a multiple of 16 per token
-  for (int c = tot + tid; c < 8 * NT * per; c += kFewWarps * 32) {
-    const int tk = c / per;
-    *reinterpret_cast<uint4 *>(sm + tk * pitch + 16 * (c - tk * per)) = make_uint4(0, 0, 0, 0);
-  }
-  if constexpr (sizeof(XT) == 1) {
-#pragma unroll 4
-    for (int c = tid; c < tot; c += kFewWarps * 32) {
-      const int tk = c / per, k = 8 * (c - tk * per);
-      const XT *x = static_cast<const XT *>(p.x) + (long long)tk * p.ldx + (long long)g * p.K + k;
-      const uint2 u = k < p.K ? *reinterpret_cast<const uint2 *>(x) : make_uint2(0, 0);
-      *reinterpret_cast<uint4 *>(sm + tk * pitch + 2 * k) =
-          make_uint4(e4m3x2_f16x2(u.x), e4m3x2_f16x2(u.x >> 16), e4m3x2_f16x2(u.y), e4m3x2_f16x2(u.y >> 16));
-    }
-    if (tid < p.T) xd[tid] = p.x_scale[tid];
-  } else {
-    // the bf16 values first, then in place once each token's largest is known
-    __shared__ uint32_t amax[8 * NT];                     // |x| as bits, in the order of the values
-    if (tid < 8 * NT) amax[tid] = 0u;
-    __syncthreads();
-#pragma unroll 8
-    for (int c = tid; c < tot; c += kFewWarps * 32) {
-      const int tk = c / per, k = 8 * (c - tk * per);
-      const XT *x = static_cast<const XT *>(p.x) + (long long)tk * p.ldx + (long long)g * p.K + k;
-      const uint4 u = k < p.K ? *reinterpret_cast<const uint4 *>(x) : make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4 *>(sm + tk * pitch + 2 * k) = u;
-      uint32_t am = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
-                             __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
-      am = max(am & 0xFFFFu, am >> 16);
-      am = __reduce_max_sync(0xFFFFu << (lane & 16), am);   // 16 lanes of one token
-      if ((lane & 15) == 0) atomicMax(&amax[tk], am);
-    }
-    __syncthreads();
-#pragma unroll 4
-    for (int c = tid; c < tot; c += kFewWarps * 32) {
-      const int tk = c / per, k = 8 * (c - tk * per);
-      // 2^e <= the largest value < 2^(e + 1), e at least -110 so that 2^(14 - e) and its inverse are normal
-      const float up = pow2f(14 - max((int)(amax[tk] >> 7) - 127, -110));
-      uint8_t *o = sm + tk * pitch + 2 * k;
-      float f[8];
-      load8(reinterpret_cast<const __nv_bfloat16 *>(o), f);
-      __half2 h[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i] * up, f[2 * i + 1] * up);
-      *reinterpret_cast<uint4 *>(o) = *reinterpret_cast<const uint4 *>(h);
-    }
-    if (tid < p.T) xd[tid] = pow2f(max((int)(amax[tid] >> 7) - 127, -110) - 14);
-  }
-  __syncthreads();
-
-  float acc[MT][NT][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
-
-  auto multiply = [&](int b, const uint4 (&v)[MT][2], const uint32_t (&sc)[MT][2]) {
-    uint32_t s2[MT][2], t2[MT][2], w[MT][2][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        s2[m][h] = e4m3_f16x2_dup(sc[m][h]);
-        t2[m][h] = CODE == HCA_W4_INT4 ? hmul2_u32(s2[m][h], 0xA400A400u) : 0u;
-        // lanes 2 and 3 of a quad take their words in pairwise swapped order: with it the four lanes'
-        // reads of x fall into four different 16-byte bank groups
-        const uint4 &q = v[m][h];
-        w[m][h][0] = t & 2 ? q.y : q.x;
-        w[m][h][1] = t & 2 ? q.x : q.y;
-        w[m][h][2] = t & 2 ? q.w : q.z;
-        w[m][h][3] = t & 2 ? q.z : q.w;
-      }
-    const uint8_t *xb = sm + gr * pitch + (b * 128 + 32 * t) * 2;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = j ^ (t >> 1);
-      uint4 xv[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) xv[n] = *reinterpret_cast<const uint4 *>(xb + n * 8 * pitch + 16 * c);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint32_t f[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) w4_decode8<CODE>(w[m][h][j], s2[m][h], t2[m][h], f[h]);
-        const uint32_t a0[4] = {f[0][0], f[1][0], f[0][1], f[1][1]}, a1[4] = {f[0][2], f[1][2], f[0][3], f[1][3]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_f16(acc[m][n], a0, xv[n].x, xv[n].y);
-          mma_f16(acc[m][n], a1, xv[n].z, xv[n].w);
-        }
-      }
-    }
-  };
-  for (int b = b0; b < b1; b += PF) {
-#pragma unroll
-    for (int u = 0; u < PF; ++u) {
-      if (b + u >= b1) break;
-      multiply(b + u, v[u], sc[u]);
-      if (b + u + PF < b1) load(b + u + PF, v[u], sc[u]);
-    }
-  }
-
-  // ---- parts of the KS warps of one row set, added in order
-  if (KS > 1) {
-    __syncthreads();                       // x has been read
-    float *red = reinterpret_cast<float *>(sm) + warp * (MT * NT * 128);
-    if (ks > 0) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          *reinterpret_cast<float4 *>(red + (m * NT + j) * 128 + 4 * lane) =
-              make_float4(acc[m][j][0], acc[m][j][1], acc[m][j][2], acc[m][j][3]);
-    }
-    __syncthreads();
-    if (ks > 0) return;
-    for (int z = 1; z < KS; ++z)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const float4 a = *reinterpret_cast<const float4 *>(red + z * (MT * NT * 128) + (m * NT + j) * 128 + 4 * lane);
-          acc[m][j][0] += a.x; acc[m][j][1] += a.y; acc[m][j][2] += a.z; acc[m][j][3] += a.w;
-        }
-  }
-  // accumulator i: row gr + 8 (i / 2), token 2 t + i % 2
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = nrow[h] + 16 * m;
-      if (r >= p.N) continue;
-      const float rs = __ldg(p.row_scale + (long long)g * p.N + r) * (CODE == HCA_W4_INT4 ? 512.f : 1.f);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int tk = 8 * j + 2 * t + i;
-          if (tk < p.T)
-            Elt<OT>::store(static_cast<OT *>(p.out) + (long long)tk * p.ldo + (long long)g * p.N + r,
-                           acc[m][j][2 * h + i] * rs * xd[tk]);
-        }
-    }
 }
 
 // ---------------------------------------------------------------- the product
@@ -367,7 +173,8 @@ W4Work w4_work(const W4Params &p, int tn) {
   w.base = w.U / w.gran / w.G;
   w.rem = w.U / w.gran - w.base * w.G;
   const int run = (w.base + (w.rem > 0)) * w.gran;   // the longest
-  w.x = w.ntt > 1 ? kRing : run <= NX ? kByUnit : p.groups == 1 && w.nk <= NX ? kByBlock : kRing;
+  const bool block = p.groups == 1 && w.nk <= NX;
+  w.x = w.ntt > 1 ? kRing : block && w.nk <= run ? kByBlock : run <= NX ? kByUnit : block ? kByBlock : kRing;
   return w;
 }
 constexpr int kMaxT = 4096;               // tokens of one launch
@@ -425,9 +232,10 @@ __device__ __forceinline__ void w4_dec_sync() { asm volatile("bar.sync 1, %0;" :
 // of a unit at a time, a lane 8 channels.  bf16 values whose token has its
 // largest in [1, 2^15) (among the units staged here) are stored as they are;
 // a token outside that range is stored again, scaled.
-template <int TN, typename XT>
+template <int TN, int CODE, typename XT>
 __device__ __forceinline__ void w4_stage_x(const W4Params &p, const W4Work &wk, int u0, int units, uint8_t *xs, float *xd,
                                            uint32_t *amax) {
+  constexpr int kBatch = 8;      // loads on their way before the first store
   const int w = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, tid = threadIdx.x - 64;
   // unit un of the run: channels from k of group g (a run may pass into further tiles and groups)
   int first = 0, g0 = 0, t0 = 0;
@@ -453,31 +261,49 @@ __device__ __forceinline__ void w4_stage_x(const W4Params &p, const W4Work &wk, 
     *reinterpret_cast<uint4 *>(xs + un * W4Layout<TN>::kX + (lane / 8) * (TN * 128) + sw128_off(row, lane % 8)) = h;
   };
   if constexpr (sizeof(XT) == 1) {
-#pragma unroll 4
-    for (int c = w; c < units * TN; c += kDecWarps) {
-      const XT *x = source(c / TN, c % TN);
-      const uint2 u = x ? *reinterpret_cast<const uint2 *>(x) : make_uint2(0, 0);
-      store(c / TN, c % TN,
-            make_uint4(e4m3x2_f16x2(u.x), e4m3x2_f16x2(u.x >> 16), e4m3x2_f16x2(u.y), e4m3x2_f16x2(u.y >> 16)));
+#pragma unroll 1
+    for (int c = w; c < units * TN; c += kBatch * kDecWarps) {
+      uint2 u[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int cj = c + j * kDecWarps;
+        const XT *x = cj < units * TN ? source(cj / TN, cj % TN) : nullptr;
+        u[j] = x ? __ldg(reinterpret_cast<const uint2 *>(x)) : make_uint2(0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int cj = c + j * kDecWarps;
+        if (cj < units * TN) store(cj / TN, cj % TN, w4_x8<CODE>(u[j]));
+      }
     }
     if (tid < p.T) xd[tid] = p.x_scale[tid];
   } else {
     if (tid < TN) amax[tid] = 0u;                  // |x| as bits, in the order of the values
     w4_dec_sync();
     auto f16 = [](const uint4 &u, float up) {
-      __half2 h[4] = {__floats2half2_rn(bf16_lo(u.x) * up, bf16_hi(u.x) * up), __floats2half2_rn(bf16_lo(u.y) * up, bf16_hi(u.y) * up),
-                      __floats2half2_rn(bf16_lo(u.z) * up, bf16_hi(u.z) * up), __floats2half2_rn(bf16_lo(u.w) * up, bf16_hi(u.w) * up)};
-      return *reinterpret_cast<const uint4 *>(h);
+      const float v[8] = {bf16_lo(u.x) * up, bf16_hi(u.x) * up, bf16_lo(u.y) * up, bf16_hi(u.y) * up,
+                          bf16_lo(u.z) * up, bf16_hi(u.z) * up, bf16_lo(u.w) * up, bf16_hi(u.w) * up};
+      return w4_x8<CODE>(v);
     };
-#pragma unroll 4
-    for (int c = w; c < units * TN; c += kDecWarps) {
-      const XT *x = source(c / TN, c % TN);
-      const uint4 u = x ? *reinterpret_cast<const uint4 *>(x) : make_uint4(0, 0, 0, 0);
-      store(c / TN, c % TN, f16(u, 1.0f));
-      uint32_t am = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
-                             __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
-      am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
-      if (lane == 0) atomicMax(&amax[c % TN], am);
+#pragma unroll 1
+    for (int c = w; c < units * TN; c += kBatch * kDecWarps) {
+      uint4 u[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int cj = c + j * kDecWarps;
+        const XT *x = cj < units * TN ? source(cj / TN, cj % TN) : nullptr;
+        u[j] = x ? __ldg(reinterpret_cast<const uint4 *>(x)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int cj = c + j * kDecWarps;
+        if (cj >= units * TN) break;
+        store(cj / TN, cj % TN, f16(u[j], 1.0f));
+        uint32_t am = __vmaxu2(__vmaxu2(u[j].x & 0x7FFF7FFFu, u[j].y & 0x7FFF7FFFu),
+                               __vmaxu2(u[j].z & 0x7FFF7FFFu, u[j].w & 0x7FFF7FFFu));
+        am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
+        if (lane == 0 && am) atomicMax(&amax[cj % TN], am);
+      }
     }
     w4_dec_sync();
     // 2^e <= the largest value < 2^(e + 1), e at least -110 so that 2^(14 - e) and its inverse are normal
@@ -632,7 +458,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
     if (wk.x != kRing) {
       pdl_wait();   // x of the kernel before
       const int units = wk.x == kByUnit ? n : wk.nk;
-      w4_stage_x<TN, XT>(p, wk, u0, units, smem + L::x_off, xds, reinterpret_cast<uint32_t *>(xds + 64));
+      w4_stage_x<TN, CODE, XT>(p, wk, u0, units, smem + L::x_off, xds, reinterpret_cast<uint32_t *>(xds + 64));
       fence_proxy_async();     // the tensor cores read it through the async proxy
       __syncwarp();
       if (lane == 0)
@@ -650,14 +476,12 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       if (!mbar_wait_fast(bar(bars->c_full[st]), cph, p.status)) break;
       const uint8_t *stage = smem + st * L::kStage;
       const uint4 v0 = *reinterpret_cast<const uint4 *>(stage + o0), v1 = *reinterpret_cast<const uint4 *>(stage + o1);
-      const uint32_t sa = e4m3_f16x2_dup(stage[s0]), sb = e4m3_f16x2_dup(stage[s1]);
+      const uint32_t ba = stage[s0], bb = stage[s1];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars->c_empty[st]));
-      uint32_t na = 0, nb = 0;
-      if constexpr (CODE == HCA_W4_INT4) {   // times -2^-6: -8 of the byte's units
-        na = hmul2_u32(sa, 0xA400A400u);
-        nb = hmul2_u32(sb, 0xA400A400u);
-      }
+      uint32_t sa, sb, na, nb;
+      w4_scale<CODE>(ba, sa, na);
+      w4_scale<CODE>(bb, sb, nb);
       uint32_t f0[16], f1[16];
       w4_decode<CODE>(v0, sa, na, f0);
       w4_decode<CODE>(v1, sb, nb, f1);
@@ -710,13 +534,16 @@ __global__ void __launch_bounds__(kW4Threads, 1)
         uint32_t v[8], v1[8];
         tmem_ld_32x32b_x8(td + d * 64 + j0, v);
         tmem_ld_32x32b_x8(td + d * 64 + L::kSecond + j0, v1);
+        float x[8], a[8];                   // read before the first store, which might be to the same memory for all
+        load8(xds + j0, x);                 // that the compiler knows
         tmem_ld_wait();
 #pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = (__uint_as_float(v[j]) + __uint_as_float(v1[j])) * x[j] * rs;
+#pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float a = (__uint_as_float(v[j]) + __uint_as_float(v1[j])) * xds[j0 + j] * rs;
           if (j0 + j < nt) {
-            if (!whole) *pp = a;
-            else if (o < p.N) Elt<OT>::store(po, a);
+            if (!whole) *pp = a[j];
+            else if (o < p.N) Elt<OT>::store(po, a[j]);
           }
           pp += kTileN;
           po += p.ldo;
@@ -765,41 +592,6 @@ __global__ void __launch_bounds__(kTileN) w4_join_kernel(W4Params p, W4Work wk, 
     if (j < nt)
       Elt<OT>::store(static_cast<OT *>(p.out) + (long long)(t0 + tl + j) * p.ldo + (long long)g * p.N + o,
                      acc[j] * rs);
-}
-
-// Up to 32 tokens whose x fits; the larger products of many tokens belong to
-// the tensor-memory kernel.
-bool w4_few(const W4Params &p) {
-  const int Kp = (p.K + 127) / 128 * 128, T8 = (p.T + 7) / 8 * 8;
-  return p.T <= 32 && (long long)T8 * Kp <= kFewElems && (long long)p.groups * p.N * p.K <= (4 << 20);
-}
-template <int MT, int NT, int CODE, typename XT, typename OT>
-int launch_few_t(const W4Params &p, cudaStream_t s) {
-  const int Kp = (p.K + 127) / 128 * 128;
-  // warps per row set: as many as keep the grid within two blocks per SM, at most one per 128 channels
-  int KS = kFewWarps;
-  auto blocks = [&](int ks) { return (p.N + 16 * MT * (kFewWarps / ks) - 1) / (16 * MT * (kFewWarps / ks)); };
-  while (KS > 1 && ((long long)blocks(KS) * p.groups > 2 * num_sms() || Kp / 128 < KS)) KS /= 2;
-  const size_t smem = std::max<size_t>((size_t)8 * NT * few_pitch(Kp), KS > 1 ? (size_t)kFewWarps * MT * NT * 512 : 0);
-  static std::atomic<bool> attr_dev[kMaxDevices];
-  std::atomic<bool> &attr = attr_dev[device_slot()];
-  if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(w4_few_kernel<MT, NT, CODE, XT, OT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kFewElems * 2 + 32 * 32);
-    if (e != cudaSuccess) return fail(HCA_ERR_CUDA, "w4_linear smem attribute: %s", cudaGetErrorString(e));
-    attr = true;
-  }
-  return HCA_LAUNCH("w4_linear", s, w4_few_kernel<MT, NT, CODE, XT, OT><<<dim3(blocks(KS), p.groups), kFewWarps * 32, smem, s>>>(p, KS, Kp));
-}
-template <int CODE, typename XT, typename OT>
-int launch_few_c(const W4Params &p, cudaStream_t s) {
-  if (p.T <= 8) return launch_few_t<1, 1, CODE, XT, OT>(p, s);
-  if (p.T <= 16) return launch_few_t<2, 2, CODE, XT, OT>(p, s);
-  return launch_few_t<2, 4, CODE, XT, OT>(p, s);
-}
-template <typename XT, typename OT>
-int launch_few(const W4Params &p, cudaStream_t s) {
-  return p.code == HCA_W4_E2M1 ? launch_few_c<HCA_W4_E2M1, XT, OT>(p, s) : launch_few_c<HCA_W4_INT4, XT, OT>(p, s);
 }
 
 template <typename... KArgs, typename... Args>
@@ -853,7 +645,7 @@ int launch_w4_t(const W4Params &p, cudaStream_t s) {
                         (uint64_t)l.Kp * 2, 64, TN, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc) return rc;
   if (wk.x == kRing) {
-    rc = HCA_LAUNCH("w4_x", s, w4_x_kernel<XT><<<(unsigned)p.groups * p.T, 256, 0, s>>>(p, xh, xd, l.Kp));
+    rc = HCA_LAUNCH("w4_x", s, w4_x_kernel<CODE, XT><<<(unsigned)p.groups * p.T, 256, 0, s>>>(p, xh, xd, l.Kp));
     if (rc) return rc;
   } else {
     tmX = tmC;      // not used
@@ -924,7 +716,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(const T *__restrict__ 
 }  // namespace
 
 size_t w4_workspace_bytes(const W4Params &p) {
-  if (p.T <= 0 || w4_few(p)) return 0;
+  if (p.T <= 0) return 0;
   W4Params c = p;
   c.T = std::min(p.T, kMaxT);
   const size_t most = w4_ws(c).bytes;
@@ -934,10 +726,6 @@ size_t w4_workspace_bytes(const W4Params &p) {
 
 int launch_w4_linear(const W4Params &p, hca_dtype xd, hca_dtype od, cudaStream_t s) {
   if (p.T == 0) return HCA_OK;
-  if (w4_few(p)) {
-    if (xd == HCA_BF16) return od == HCA_F32 ? launch_few<__nv_bfloat16, float>(p, s) : launch_few<__nv_bfloat16, __nv_bfloat16>(p, s);
-    return od == HCA_F32 ? launch_few<unsigned char, float>(p, s) : launch_few<unsigned char, __nv_bfloat16>(p, s);
-  }
   // many tokens: runs of at most kMaxT, so that unit numbers stay within 31 bits
   W4Params c = p;
   for (int t0 = 0; t0 < p.T; t0 += kMaxT) {
