@@ -5,6 +5,30 @@
 // max(0, pos - w + 1) .. pos and the compressed entries (listed, or all that
 // are visible); z_j = scale q_h . row_j; o_h = sum_j e^{z_j} row_j /
 // (sum_j e^{z_j} + e^{sink_h}); the last rd dims of o_h rotated by -pos.
+//
+// Keys are taken 64 at a time, a sequence's window tiles first.  The tiles of
+// all sequences form one list, and every CTA takes an equal run of it, so that
+// ragged lengths cost nothing and few sequences still fill the GPU; the runs
+// follow from the positions on the device, which each CTA sums up itself.  A
+// sequence inside one run is finished there; one that was cut leaves
+// unnormalised fp32 parts, which fp4_combine_kernel joins in their order.
+//
+// Per tile (tcgen05, the sequence's n_h <= 64 heads as the MMA's M = 64):
+//   8 loader warps   records of a tile one tile ahead in registers, codes to
+//                    bf16 (exact: two significant bits and a power of two) in
+//                    a 128B-swizzled shared-memory tile that serves as K
+//                    (K-major) and V (MN-major); skipped keys as zero rows
+//   1 MMA warp       S = Q K^T (Q in tensor memory, the A operand), O += P V;
+//                    S of the next tile is issued before P V of this one
+//   4 softmax warps  S from tensor memory, running maximum moved only when it
+//                    grows by more than 2^8, P in bf16 (its rounding, 2^-8 of
+//                    p, is that of the bf16 output; sums and statistics fp32)
+// Bound: M = 64 uses half the tensor pipe, 2048 cycles per tile at c = 512,
+// against 900 for the conversion and 64 x 368 bytes of HBM (1000 cycles at an
+// SM's share).  With few tiles per CTA the fixed parts (first loads, fill of
+// the pipeline, joining) are most of the time.
+#include <algorithm>
+
 #include "internal.h"
 #include "lowbit.cuh"
 
@@ -12,125 +36,719 @@ namespace hca {
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int KT = 64;
+constexpr int kMmaWarp = 4, kLoad0 = 5, kLoadWarps = 8;
+constexpr int kThreads = (kLoad0 + kLoadWarps) * 32;
+constexpr uint32_t kTileBytes = 64 * 128;   // 64 rows x 128 B: one 64-channel block of a tile
+constexpr int SP = 2;                        // S and P buffers
+
+// Launch-time sizes beside the call's parameters.
+struct Fp4Plan {
+  int G;                   // CTAs
+  FastDiv fd_m, fd_cap;
+  float *part_o;           // [2 G][n_h][c]
+  float2 *part_ml;         // [2 G][n_h]
+  int4 *meta;              // [B]: first and last CTA of a cut sequence and the first one's slot; x < 0: finished
+};
+
 // The key set of sequence b.
 struct Fp4Keys {
-  int pos, nw, V, n;   // position, window rows, visible entries the cache can hold, key slots (idx slots included)
+  int pos, nw, V, ne;   // position, window rows, visible entries the cache can hold, entry slots (listed or V)
+  int nwt, nt;          // window tiles, all tiles
 };
-__device__ __forceinline__ Fp4Keys fp4_keys(const AttendFp4Params &p, int b) {
+__device__ __forceinline__ Fp4Keys fp4_keys(const AttendFp4Params &p, const Fp4Plan &pl, int b) {
   Fp4Keys k;
   k.pos = min(__ldg(p.positions + b), p.max_pos);
   if (k.pos < 0) {
     k.pos = -1;
-    k.nw = k.V = k.n = 0;
+    k.nw = k.V = k.ne = k.nwt = k.nt = 0;
     return k;
   }
   k.nw = min(p.w, k.pos + 1);
   const long long room = p.pages ? (long long)p.max_pages * p.cap : (long long)p.cap;
-  k.V = (int)min((long long)((k.pos + 1) / p.m), room);
-  k.n = k.nw + (p.idx ? p.k : k.V);
+  k.V = (int)min((long long)fdiv(k.pos + 1, pl.fd_m), room);
+  k.ne = p.idx ? p.k : k.V;
+  k.nwt = (k.nw + KT - 1) / KT;
+  k.nt = k.nwt + (k.ne + KT - 1) / KT;
   return k;
 }
-// Record of compressed key slot j (0 <= j < n - nw); NULL = skipped.
-__device__ __forceinline__ const unsigned char *fp4_record(const AttendFp4Params &p, int b, const Fp4Keys &k, int j) {
-  const int e = p.idx ? __ldg(p.idx + (long long)b * p.k + j) : j;
-  if (e < 0 || e >= k.V) return nullptr;
-  long long row;
-  if (p.pages) {
-    const int pg = __ldg(p.pages + (long long)b * p.max_pages + e / p.cap);
-    if (pg < 0 || pg >= p.n_pages) return nullptr;
-    row = (long long)pg * p.cap + e % p.cap;
-  } else {
-    row = (long long)b * p.cap + e;
-  }
-  return p.rows + row * p.rec;
+
+template <int C>
+struct Fp4Layout {
+  static constexpr int NKB = C / 64;
+  static constexpr int NS = C == 512 ? 3 : C == 256 ? 6 : 8;    // key-tile stages
+  static constexpr uint32_t p_off = NS * NKB * kTileBytes;
+  static constexpr uint32_t bar_off = p_off + SP * kTileBytes;
+  static constexpr uint32_t mask_off = bar_off + 512;            // [NS][2] uint32: keys of a stage
+  static constexpr uint32_t run_off = mask_off + 64;             // [8] int: this CTA's run
+  static constexpr uint32_t sum_off = run_off + 64;              // [16] long long: prefix sums
+  static constexpr uint32_t rope_off = sum_off + 128;            // [256] float2
+  static constexpr uint32_t bytes = rope_off + 2048 + 1024;
+  static_assert(bytes <= 227 * 1024, "shared memory");
+  // tensor memory: O in lane-half 0, columns [0, C); in lane-half 1 S buffers
+  // at [0, 128) and Q (bf16, two per column) at [128, 128 + C / 2)
+  static constexpr uint32_t q_col = SP * KT;
+};
+
+struct Fp4Bars {
+  uint64_t q_full, q_empty, o_empty, kv_full[8], kv_empty[8], s_full[SP], s_empty[SP], p_full[SP], pv_done[SP];
+  uint32_t tmem;
+};
+
+// This CTA's run of tiles: from tile `j0` of sequence `b0`, `n` tiles; `before`
+// = tiles of all sequences before the run's first tile.
+struct Fp4Run {
+  int b0, j0;
+  long long n, before, base, rem;
+};
+// Runs are base or base + 1 tiles long, the first rem ones the longer.
+__device__ __forceinline__ int fp4_cta_of(const Fp4Run &r, long long tile) {
+  const long long cut = r.rem * (r.base + 1);
+  return (int)(tile < cut ? tile / (r.base + 1) : r.rem + (tile - cut) / r.base);
 }
 
-constexpr int kSimpleTile = 16;
+// Walks the pieces of a run: tiles [j, j + cnt) of sequence b.
+struct Fp4Walk {
+  int b, j, cnt;
+  long long left;
+  Fp4Keys k;
+};
+__device__ __forceinline__ Fp4Walk fp4_walk(const Fp4Run &r) {
+  Fp4Walk w;
+  w.b = r.b0 - 1;
+  w.j = r.j0;
+  w.cnt = 0;
+  w.left = r.n;
+  return w;
+}
+// The next piece; false at the end of the run.
+__device__ __forceinline__ bool fp4_next(const AttendFp4Params &p, const Fp4Plan &pl, const Fp4Run &r, Fp4Walk &w) {
+  if (w.left <= 0) return false;
+  do {
+    if (++w.b >= p.B) return false;
+    w.k = fp4_keys(p, pl, w.b);
+  } while (w.k.nt == 0);
+  w.j = w.b == r.b0 ? r.j0 : 0;
+  w.cnt = (int)min((long long)(w.k.nt - w.j), w.left);
+  w.left -= w.cnt;
+  return true;
+}
 
-// One block per (head, sequence): 16 keys at a time in shared memory, a warp
-// per two keys' logits, a thread per two channels' output.
-__global__ void __launch_bounds__(256) attend_fp4_simple_kernel(AttendFp4Params p) {
-  extern __shared__ float sm[];
-  float *kv = sm, *q = sm + kSimpleTile * p.c, *z = q + p.c;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Fp4Keys ks = fp4_keys(p, b);
-  const int nq = p.c - p.rd;
-  const __nv_bfloat16 *qp = p.q + ((long long)b * p.n_h + h) * p.c;
-  for (int i = tid; i < p.c; i += 256) q[i] = __bfloat162float(qp[i]);
-  const float sink = p.sink ? p.sink[h] * 1.4426950408889634f : -INFINITY;
-  float m = sink, l = p.sink ? 1.f : 0.f, o[2] = {0.f, 0.f};
-  for (int j0 = 0; j0 < ks.n; j0 += kSimpleTile) {
-    __syncthreads();
-    for (int i = tid; i < kSimpleTile * p.c; i += 256) {
-      const int jj = i / p.c, ch = i - jj * p.c, j = j0 + jj;
-      float v = 0.f;
-      if (j < ks.nw) {
-        const int tok = ks.pos - ks.nw + 1 + j;
-        v = __bfloat162float(p.kv_win[((long long)b * p.w + tok % p.w) * p.c + ch]);
-      } else if (j < ks.n) {
-        const unsigned char *r = fp4_record(p, b, ks, j - ks.nw);
-        if (r) {
-          if (ch < nq) {
-            uint32_t f[4];
-            e2m1x8_f16(reinterpret_cast<const uint32_t *>(r)[ch / 8], f);
-            const uint32_t pr = ch & 4 ? (ch & 2 ? f[3] : f[2]) : (ch & 2 ? f[1] : f[0]);
-            __half_raw h;
-            h.x = (unsigned short)(ch & 1 ? pr >> 16 : pr & 0xFFFFu);
-            v = __half2float(__half(h)) * pow2f(max((int)r[nq / 2 + 2 * p.rd + ch / 32], 1) - 127);
-          } else {
-            v = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(r + nq / 2)[ch - nq]);
+// ---------------------------------------------------------------- loaders
+// Where the loader threads find a tile: thread (key, group) of an entry tile
+// its record (row < 0: skipped), of a window tile the first token.
+struct Fp4Tile {
+  int b, win0, wcnt;       // window tile: sequence, first token, rows; win0 < 0: entry tile
+  int e;                   // entry of this thread's key, -1: none
+};
+
+template <int C>
+__device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan &pl, const Fp4Run &run, uint8_t *smem,
+                                         Fp4Bars *bars) {
+  using L = Fp4Layout<C>;
+  const int pt = threadIdx.x - kLoad0 * 32, lw = pt >> 5, lane = pt & 31;
+  const int kk = (lw & 1) * 32 + lane, grp = lw >> 1;          // key of the tile, quarter of the record
+  const int nq = C - p.rd, units = nq / 32, rch = p.rd / 8;     // 16-byte code units, 16-byte RoPE chunks
+  const int per = units <= 4 ? 1 : units <= 8 ? 2 : 4;          // units of this thread: u0 .. u0 + per - 1
+  const int u0 = grp * per;
+  const int eoff = nq / 2 + 2 * p.rd;
+  const uint32_t sbase = smem_u32(smem);
+
+  Fp4Walk w = fp4_walk(run);
+  int t = 0;                                                     // next tile of the piece
+  // tile descriptors in order; the entry index (a load) is resolved as early as possible
+  auto next_tile = [&](Fp4Tile &x) -> bool {
+    if (t == w.cnt) {
+      if (!fp4_next(p, pl, run, w)) return false;
+      t = 0;
+    }
+    const int j = w.j + t++;
+    x.b = w.b;
+    x.win0 = -1;
+    x.e = -1;
+    if (j < w.k.nwt) {
+      x.win0 = w.k.pos - w.k.nw + 1 + j * KT;
+      x.wcnt = min(KT, w.k.nw - j * KT);
+    } else {
+      const int s = (j - w.k.nwt) * KT + kk;
+      if (s < w.k.ne) {
+        x.e = p.idx ? __ldg(p.idx + (long long)w.b * p.k + s) : s;
+        if (x.e >= w.k.V) x.e = -1;
+      }
+    }
+    return true;
+  };
+  // record of the tile's key: index of its row, -1 = skipped
+  auto row_of = [&](const Fp4Tile &x) -> long long {
+    if (x.win0 >= 0 || x.e < 0) return -1;
+    if (!p.pages) return (long long)x.b * p.cap + x.e;
+    const int pi = fdiv(x.e, pl.fd_cap), pg = __ldg(p.pages + (long long)x.b * p.max_pages + pi);
+    return pg >= 0 && pg < p.n_pages ? (long long)pg * p.cap + (x.e - pi * p.cap) : -1;
+  };
+  struct Data {
+    uint4 c[4], r[2];
+    uint32_t e;
+  };
+  auto fetch = [&](long long row, Data &d) {
+    const unsigned char *rp = p.rows + row * p.rec;
+    const bool on = row >= 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      d.c[i] = on && i < per && u0 + i < units ? __ldg(reinterpret_cast<const uint4 *>(rp) + u0 + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      d.r[i] = on && grp + 4 * i < rch ? __ldg(reinterpret_cast<const uint4 *>(rp + nq / 2) + grp + 4 * i) : make_uint4(0, 0, 0, 0);
+    d.e = 0u;
+    if (on && u0 < units) {       // u0 is a multiple of per, and the record padded to 16 bytes
+      if (per == 4) d.e = __ldg(reinterpret_cast<const uint32_t *>(rp + eoff + u0));
+      else if (per == 2) d.e = __ldg(reinterpret_cast<const unsigned short *>(rp + eoff + u0));
+      else d.e = __ldg(rp + eoff + u0);
+    }
+  };
+
+  Fp4Tile a, n1, n2;
+  bool h0 = next_tile(a), h1 = h0 && next_tile(n1), h2 = h1 && next_tile(n2);
+  long long row0 = h0 ? row_of(a) : -1, row1 = h1 ? row_of(n1) : -1;
+  Data d0, d1;
+  if (h0) fetch(row0, d0);
+  int st = 0;
+  uint32_t ph = 1;
+  while (h0) {
+    // one tile ahead its records, two its rows, three its entries
+    if (h1) fetch(row1, d1);
+    const long long row2 = h2 ? row_of(n2) : -1;
+    Fp4Tile n3;
+    const bool h3 = h2 && next_tile(n3);
+
+    if (!mbar_wait_fast(smem_u32(&bars->kv_empty[st]), ph, p.status)) break;
+    uint8_t *tile = smem + st * L::NKB * kTileBytes;
+    uint32_t *mask = reinterpret_cast<uint32_t *>(smem + L::mask_off) + 2 * st;
+    if (a.win0 >= 0) {
+      // window rows, 16-byte chunks in the order of the row
+      constexpr int CPR = C / 8, RPP = kLoadWarps * 32 / CPR;
+      const int chunk = pt % CPR;
+      const uint32_t dst = sbase + st * L::NKB * kTileBytes + (chunk / 8) * kTileBytes;
+#pragma unroll 8
+      for (int r = pt / CPR; r < KT; r += RPP) {
+        const bool on = r < a.wcnt;
+        const __nv_bfloat16 *src = p.kv_win + ((long long)a.b * p.w + (on ? (a.win0 + r) % p.w : 0)) * C + chunk * 8;
+        cp_async16(dst + sw128_off(r, chunk % 8), src, on ? 16 : 0);
+      }
+      cp_async_arrive_noinc(smem_u32(&bars->kv_full[st]));
+      if (pt == 0) {
+        mask[0] = range_bits(0, 0, a.wcnt);
+        mask[1] = range_bits(32, 0, a.wcnt);
+        mbar_arrive(smem_u32(&bars->kv_full[st]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int u = u0 + i;                       // channels 32 u .. 32 u + 31
+        if (i >= per || u >= units) break;
+        const float sc = pow2f(max((int)((d0.e >> (8 * i)) & 255u), 1) - 127);   // byte 0: all codes are zero
+        const uint32_t wd[4] = {d0.c[i].x, d0.c[i].y, d0.c[i].z, d0.c[i].w};
+        uint8_t *dst = tile + (u / 2) * kTileBytes;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t f[4], o[4];
+          e2m1x8_f16(wd[h], f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f[q]));
+            o[q] = pack_bf16x2(v.x * sc, v.y * sc);
           }
+          *reinterpret_cast<uint4 *>(dst + sw128_off(kk, (u & 1) * 4 + h)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
-      kv[i] = v;
+      for (int i = 0, ch = grp; ch < rch; ch += 4, ++i) {
+        const int c8 = nq / 8 + ch;
+        uint4 v = i == 0 ? d0.r[0] : d0.r[1];
+        if (i > 1) v = row0 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.rows + row0 * p.rec + nq / 2) + ch) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(tile + (c8 / 8) * kTileBytes + sw128_off(kk, c8 % 8)) = v;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, row0 >= 0);
+      if (grp == 0 && lane == 0) mask[lw] = m;
+      fence_proxy_async();      // the tensor cores read the tile through the async proxy
+      mbar_arrive(smem_u32(&bars->kv_full[st]));
+      if (pt == 0) mbar_arrive(smem_u32(&bars->kv_full[st]));
     }
-    __syncthreads();
-    for (int jj = warp; jj < kSimpleTile; jj += 8) {
-      const int j = j0 + jj;
-      const bool live = j < ks.n && (j < ks.nw || fp4_record(p, b, ks, j - ks.nw));
-      float a = 0.f;
-      for (int i = lane; i < p.c; i += 32) a += q[i] * kv[jj * p.c + i];
-      a = warp_sum(a);
-      if (lane == 0) z[jj] = live ? a * p.scale * 1.4426950408889634f : -INFINITY;
+    if (++st == L::NS) {
+      st = 0;
+      ph ^= 1;
     }
-    __syncthreads();
-    float mt = m;
-    for (int jj = 0; jj < kSimpleTile; ++jj) mt = fmaxf(mt, z[jj]);
-    if (mt == -INFINITY) continue;
-    const float f = exp2f(m - mt);
-    m = mt;
-    l *= f;
-    o[0] *= f;
-    o[1] *= f;
-    for (int jj = 0; jj < kSimpleTile; ++jj) {
-      const float e = exp2f(z[jj] - m);
-      l += e;
+    a = n1;
+    n1 = n2;
+    n2 = n3;
+    row0 = row1;
+    row1 = row2;
+    d0 = d1;
+    h0 = h1;
+    h1 = h2;
+    h2 = h3;
+  }
+  cp_async_wait_all();
+}
+
+// ---------------------------------------------------------------- MMA issue
+template <int C>
+__device__ __forceinline__ void fp4_mma(const AttendFp4Params &p, const Fp4Plan &pl, const Fp4Run &run, uint32_t sbase,
+                                        Fp4Bars *bars, uint32_t tmem) {
+  using L = Fp4Layout<C>;
+  constexpr uint32_t IDESC_S = idesc_bf16(64, KT, 0, 0);
+  constexpr int NPV = C < 256 ? C : 256;
+  constexpr uint32_t IDESC_PV = idesc_bf16(64, NPV, 0, 1);
+  const uint32_t tS = tmem + (16u << 16);
+  auto bar = [&](uint64_t &b) { return smem_u32(&b); };
+  int ks = 0, vs = 0;                     // stage of the next S and of the next P V
+  uint32_t kph = 0, gs = 0, gv = 0;       // tiles issued so far
+  int npiece = 0;
+  bool ok = true;
+  auto issue_pv = [&](bool first) {
+    const int st = gv % SP;
+    ok = mbar_wait_fast(bar(bars->p_full[st]), (gv / SP) & 1, p.status) &&
+         (!first || mbar_wait_fast(bar(bars->o_empty), (npiece & 1) ^ 1, p.status));
+    if (!ok) return;
+    tc_fence_after();
+    if (elect_one()) {
+      const uint64_t pd = sdesc_sw128(sbase + L::p_off + st * kTileBytes, 16, 1024);
+      const uint64_t vd = sdesc_sw128(sbase + vs * L::NKB * kTileBytes, kTileBytes, 1024);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (2 * tid + i < p.c) o[i] += e * kv[jj * p.c + 2 * tid + i];
+      for (int kk = 0; kk < KT / 16; ++kk)
+#pragma unroll
+        for (int nh = 0; nh < C / NPV; ++nh)
+          umma_bf16(tmem + nh * NPV, pd + ((kk * 32) >> 4), vd + ((nh * (NPV / 64) * kTileBytes + kk * 16 * 128) >> 4),
+                    IDESC_PV, first && kk == 0 ? 0u : 1u);
+      umma_commit(bar(bars->kv_empty[vs]));
+      umma_commit(bar(bars->pv_done[st]));
+    }
+    __syncwarp();
+    if (++vs == L::NS) vs = 0;
+    ++gv;
+  };
+  for (Fp4Walk w = fp4_walk(run); ok && fp4_next(p, pl, run, w); ++npiece) {
+    ok = mbar_wait_fast(bar(bars->q_full), npiece & 1, p.status);
+    for (int j = 0; j < w.cnt && ok; ++j) {
+      const int st = gs % SP;
+      ok = mbar_wait_fast(bar(bars->kv_full[ks]), kph, p.status) &&
+           mbar_wait_fast(bar(bars->s_empty[st]), ((gs / SP) & 1) ^ 1, p.status);
+      if (!ok) break;
+      fence_proxy_async();                // window rows come by cp.async
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t kd = sdesc_sw128(sbase + ks * L::NKB * kTileBytes, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < C / 16; ++kk)
+          umma_bf16_ts(tS + st * KT, tS + L::q_col + 8 * kk, kd + (((kk / 4) * kTileBytes + (kk % 4) * 32) >> 4), IDESC_S,
+                       kk > 0 ? 1u : 0u);
+        umma_commit(bar(bars->s_full[st]));
+        if (j == w.cnt - 1) umma_commit(bar(bars->q_empty));
+      }
+      __syncwarp();
+      if (++ks == L::NS) {
+        ks = 0;
+        kph ^= 1;
+      }
+      ++gs;
+      if (j > 0) issue_pv(j == 1);
+    }
+    if (ok) issue_pv(w.cnt == 1);
+  }
+}
+
+// sin and cos of position pos for pair i; the angle is reduced in double to
+// [-pi, pi], where the fast sine and cosine are within 2^-20.
+__device__ __forceinline__ void fp4_rope(const AttendFp4Params &p, int pos, int i, float &sn, float &cs) {
+  const double f = p.rd <= 64 ? p.rope_freq[i] : exp2(-2.0 * (double)i / (double)p.rd * log2((double)p.theta));
+  double a = (double)pos * f;
+  a -= 6.283185307179586476925286766559 * rint(a * 0.15915494309189533576888376337251);
+  __sincosf((float)a, &sn, &cs);
+}
+
+// ---------------------------------------------------------------- softmax + epilogue
+template <int C>
+__device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4Plan &pl, const Fp4Run &run, uint8_t *smem,
+                                            Fp4Bars *bars, uint32_t tmem) {
+  using L = Fp4Layout<C>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hl = lane & 15, half = lane >> 4;
+  const int r = warp * 16 + hl;           // head; the thread has keys [32 half, +32) of a tile, then half of O's columns
+  const bool live = r < p.n_h;
+  const float zs = p.scale * kLog2e;
+  const uint32_t lane_S = (uint32_t)(warp * 32 + 16) << 16, lane_O = (uint32_t)(warp * 32) << 16;
+  float2 *rope = reinterpret_cast<float2 *>(smem + L::rope_off);
+  auto bar = [&](uint64_t &b) { return smem_u32(&b); };
+  uint32_t g = 0;                         // tiles so far
+  int ks = 0, npiece = 0;
+  uint32_t kph = 0;
+  long long before = run.before;
+
+  for (Fp4Walk w = fp4_walk(run); fp4_next(p, pl, run, w); ++npiece) {
+    // ---- Q into tensor memory (the previous piece's last S has been read)
+    if (npiece > 0 && !mbar_wait_fast(bar(bars->q_empty), (npiece - 1) & 1, p.status)) return;
+    tc_fence_after();
+    {
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((long long)w.b * p.n_h + (live ? r : 0)) * C + half * (C / 2));
+      const uint32_t tq = tmem + lane_S + L::q_col;
+#pragma unroll 1
+      for (int b0 = 0; b0 < C / 16; b0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = live ? __ldg(src + b0 + x) : make_uint4(0, 0, 0, 0);
+        tmem_st_16x32bx2_x16<C / 4>(tq + 4 * b0, *reinterpret_cast<const uint32_t(*)[16]>(&v[0]));
+        tmem_st_16x32bx2_x16<C / 4>(tq + 4 * b0 + 16, *reinterpret_cast<const uint32_t(*)[16]>(&v[4]));
+      }
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(bars->q_full));
+
+    float m_used = -INFINITY, l = 0.f;    // running maximum (log2 units; -inf until a key is seen), sum of this half
+    for (int j = 0; j < w.cnt; ++j, ++g) {
+      const int st = g % SP;
+      const uint32_t ph = (g / SP) & 1;
+      // the loaders' mask of this stage
+      if (!mbar_wait_fast(bar(bars->kv_full[ks]), kph, p.status)) return;
+      const uint32_t vmask = reinterpret_cast<const uint32_t *>(smem + L::mask_off)[2 * ks + half];
+      if (++ks == L::NS) {
+        ks = 0;
+        kph ^= 1;
+      }
+      if (!mbar_wait_fast(bar(bars->s_full[st]), ph, p.status)) return;
+      tc_fence_after();
+      uint32_t sv[32];
+      tmem_ld_16x32bx2_x16<32>(tmem + lane_S + st * KT, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
+      tmem_ld_16x32bx2_x16<32>(tmem + lane_S + st * KT + 16, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars->s_empty[st]));
+      float z[32], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        z[x] = ((vmask >> x) & 1u) ? __uint_as_float(sv[x]) * zs : -INFINITY;
+        mx[x & 3] = fmaxf(mx[x & 3], z[x]);
+      }
+      float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 16));
+      bool need = false;
+      float alpha = 1.f;
+      if (tmax != -INFINITY && (m_used == -INFINITY || tmax > m_used + 8.f)) {
+        if (m_used != -INFINITY) {        // before the first key O and l are 0
+          need = true;
+          alpha = ex2_approx(m_used - tmax);
+          l *= alpha;
+        }
+        m_used = tmax;
+      }
+      if (__any_sync(0xffffffffu, need)) {
+        // rescale O once the previous tile's P V has landed
+        if (!mbar_wait_fast(bar(bars->pv_done[(g - 1) % SP]), ((g - 1) / SP) & 1, p.status)) return;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < C / 2; c0 += 16) {
+          uint32_t ov[16];
+          tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0, ov);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
+          tmem_st_16x32bx2_x16<C / 2>(tmem + lane_O + c0, ov);
+        }
+        tmem_st_wait();
+      }
+      const float m_eff = m_used == -INFINITY ? 0.f : m_used;
+      float ps[2] = {0.f, 0.f};
+      uint32_t pk[16];
+#pragma unroll
+      for (int x = 0; x < 32; x += 2) {
+        const float p0 = ex2_approx(z[x] - m_eff), p1 = ex2_approx(z[x + 1] - m_eff);
+        ps[(x >> 1) & 1] += p0 + p1;
+        pk[x / 2] = pack_bf16x2(p0, p1);
+      }
+      l += ps[0] + ps[1];
+      // P buffer st is free once the P V of two tiles ago has completed
+      if (!mbar_wait_fast(bar(bars->pv_done[st]), ph ^ 1, p.status)) return;
+      uint8_t *prow = smem + L::p_off + st * kTileBytes;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<uint4 *>(prow + sw128_off(r, half * 4 + u)) =
+            make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+      fence_proxy_async();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars->p_full[st]));
+    }
+
+    // ---- epilogue
+    const bool whole = w.cnt == w.k.nt;
+    const float ltot = l + __shfl_xor_sync(0xffffffffu, l, 16);
+    if (whole) {
+      asm volatile("bar.sync 1, 128;" ::: "memory");       // the previous table has been read
+      for (int i = threadIdx.x; i < p.rd / 2; i += 128) {
+        float sn, cs;
+        fp4_rope(p, w.k.pos, i, sn, cs);
+        rope[i] = make_float2(cs, sn);
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+    if (pl.meta && threadIdx.x == 0 && w.j == 0) {
+      // the CTA that has a sequence's first tile says who else has some
+      const long long last = before + w.k.nt - 1;
+      pl.meta[w.b] = whole ? make_int4(-1, 0, 0, 0)
+                           : make_int4(blockIdx.x, fp4_cta_of(run, last), before == run.before ? 0 : 1, 0);
+    }
+    {
+      const uint32_t gl = g - 1;
+      if (!mbar_wait_fast(bar(bars->pv_done[gl % SP]), (gl / SP) & 1, p.status)) return;
+    }
+    tc_fence_after();
+    const long long slot = 2 * blockIdx.x + (before == run.before ? 0 : 1);
+    float inv = 0.f;
+    if (m_used != -INFINITY) inv = 1.f / (ltot + (p.sink && live ? exp2f(p.sink[r] * kLog2e - m_used) : 0.f));
+    if (!whole && live && half == 0) pl.part_ml[slot * p.n_h + r] = make_float2(m_used, ltot);
+#pragma unroll 1
+    for (int c0 = 0; c0 < C / 2; c0 += 16) {
+      uint32_t ov[16];
+      tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0, ov);
+      tmem_ld_wait();
+      if (!live) continue;
+      const int col0 = half * (C / 2) + c0;
+      if (!whole) {
+        float4 *dst = reinterpret_cast<float4 *>(pl.part_o + (slot * p.n_h + r) * C + col0);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          dst[x] = make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]),
+                               __uint_as_float(ov[4 * x + 3]));
+        continue;
+      }
+      float v[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(ov[x]) * inv;
+      if (col0 >= C - p.rd) {             // rd is a multiple of 64
+        const float2 *t = rope + (col0 - (C - p.rd)) / 2;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float2 cs = t[x];
+          const float a = v[2 * x], b = v[2 * x + 1];
+          v[2 * x] = a * cs.x + b * cs.y;
+          v[2 * x + 1] = b * cs.x - a * cs.y;
+        }
+      }
+      uint32_t o[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) o[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+      uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((long long)w.b * p.n_h + r) * C + col0);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(bars->o_empty));
+    before += w.cnt;
+  }
+}
+
+template <int C>
+__global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params p, Fp4Plan pl) {
+  using L = Fp4Layout<C>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Fp4Bars *bars = reinterpret_cast<Fp4Bars *>(smem + L::bar_off);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  auto bar = [&](uint64_t &b) { return smem_u32(&b); };
+  if (threadIdx.x == 0) {
+    mbar_init(bar(bars->q_full), 4);
+    mbar_init(bar(bars->q_empty), 1);
+    mbar_init(bar(bars->o_empty), 4);
+    for (int i = 0; i < L::NS; ++i) {
+      mbar_init(bar(bars->kv_full[i]), kLoadWarps * 32 + 1);   // every thread's part of the tile, and the mask
+      mbar_init(bar(bars->kv_empty[i]), 1);
+    }
+    for (int i = 0; i < SP; ++i) {
+      mbar_init(bar(bars->s_full[i]), 1);
+      mbar_init(bar(bars->s_empty[i]), 4);
+      mbar_init(bar(bars->p_full[i]), 4);
+      mbar_init(bar(bars->pv_done[i]), 1);
+    }
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&bars->tmem), 512);
+    tmem_relinquish();
+  }
+  pdl_trigger();
+  // ---- this CTA's run: tiles of all sequences summed up, then the sequence where the run begins
+  long long *sums = reinterpret_cast<long long *>(smem + L::sum_off);
+  Fp4Run run;
+  {
+    long long mine = 0;
+    for (int b = threadIdx.x; b < p.B; b += kThreads) mine += fp4_keys(p, pl, b).nt;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    long long total = 0;
+    for (int i = 0; i < kThreads / 32; ++i) total += sums[i];
+    run.base = total / pl.G;
+    run.rem = total - run.base * pl.G;
+    run.before = blockIdx.x * run.base + min((long long)blockIdx.x, run.rem);
+    run.n = run.base + (blockIdx.x < run.rem ? 1 : 0);
+    int *at = reinterpret_cast<int *>(smem + L::run_off);
+    long long done = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      const int nt = b < p.B ? fp4_keys(p, pl, b).nt : 0;
+      long long x = nt;                   // inclusive scan over the warp
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) sums[warp] = x;
+      __syncthreads();
+      long long all = 0;
+      for (int i = 0; i < kThreads / 32; ++i) {
+        if (i == warp) x += all;
+        all += sums[i];
+      }
+      const long long first = done + x - nt;
+      if (nt > 0 && run.before >= first && run.before < first + nt) {
+        at[0] = b;
+        at[1] = (int)(run.before - first);
+      }
+      done += all;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    run.b0 = run.n > 0 ? at[0] : 0;
+    run.j0 = run.n > 0 ? at[1] : 0;
+  }
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
+
+  if (warp >= kLoad0) {
+    fp4_load<C>(p, pl, run, smem, bars);
+  } else if (warp == kMmaWarp) {
+    fp4_mma<C>(p, pl, run, smem_u32(smem), bars, tmem);
+  } else {
+    fp4_softmax<C>(p, pl, run, smem, bars, tmem);
+    // sequences without keys: zeros
+    for (int b = blockIdx.x; b < p.B; b += pl.G) {
+      if (fp4_keys(p, pl, b).nt) continue;
+      for (int i = threadIdx.x; i < p.n_h * C / 8; i += 128)
+        reinterpret_cast<uint4 *>(p.o + (long long)b * p.n_h * C)[i] = make_uint4(0, 0, 0, 0);
+      if (pl.meta && threadIdx.x == 0) pl.meta[b] = make_int4(-1, 0, 0, 0);
     }
   }
-  if (2 * tid >= p.c) return;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  o[0] *= inv;
-  o[1] *= inv;
-  if (2 * tid >= nq && ks.pos >= 0) {
-    float si, co;
-    rope_sincos_tab(p.rope_freq, ks.pos, (2 * tid - nq) / 2, p.rd, p.theta, &si, &co);
-    const float a = o[0] * co + o[1] * si, c = o[1] * co - o[0] * si;
-    o[0] = a;
-    o[1] = c;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Cut sequences: o = sum_i 2^(m_i - M) O_i / (sum_i 2^(m_i - M) l_i +
+// 2^(sink - M)) over the parts in their order, rotated.  A thread has 4
+// channels of a head; a block 512 / c heads.
+__global__ void __launch_bounds__(128) fp4_combine_kernel(AttendFp4Params p, Fp4Plan pl) {
+  const int per = p.c / 4, b = blockIdx.x, h = blockIdx.y * (128 / per) + threadIdx.x / per;
+  const int col = 4 * (threadIdx.x % per);
+  pdl_wait();
+  const int4 meta = pl.meta[b];
+  if (meta.x < 0 || h >= p.n_h) return;
+  const float sink = p.sink ? p.sink[h] * kLog2e : -INFINITY;
+  auto slot = [&](int c) { return (long long)(2 * c + (c == meta.x ? meta.z : 0)) * p.n_h + h; };
+  float M = sink;
+#pragma unroll 4
+  for (int c = meta.x; c <= meta.y; ++c) M = fmaxf(M, pl.part_ml[slot(c)].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M != -INFINITY) {
+    float den = exp2f(sink - M);
+#pragma unroll 4
+    for (int c = meta.x; c <= meta.y; ++c) {
+      const float2 ml = pl.part_ml[slot(c)];
+      const float4 o = *reinterpret_cast<const float4 *>(pl.part_o + slot(c) * p.c + col);
+      const float f = exp2f(ml.x - M);    // 0 for a part without keys
+      den += f * ml.y;
+      acc.x += f * o.x; acc.y += f * o.y; acc.z += f * o.z; acc.w += f * o.w;
+    }
+    const float inv = 1.f / den;
+    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
   }
-  reinterpret_cast<uint32_t *>(p.o + ((long long)b * p.n_h + h) * p.c)[tid] = pack_bf16x2(o[0], o[1]);
+  if (col >= p.c - p.rd) {
+    const int pos = min(__ldg(p.positions + b), p.max_pos), i = (col - (p.c - p.rd)) / 2;
+    float s0, c0, s1, c1;
+    fp4_rope(p, pos, i, s0, c0);
+    fp4_rope(p, pos, i + 1, s1, c1);
+    acc = make_float4(acc.x * c0 + acc.y * s0, acc.y * c0 - acc.x * s0, acc.z * c1 + acc.w * s1, acc.w * c1 - acc.z * s1);
+  }
+  *reinterpret_cast<uint2 *>(p.o + ((long long)b * p.n_h + h) * p.c + col) =
+      make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+}
+
+// CTAs of a call: the budget, no more than there can be tiles; ne: entry slots of a sequence.
+int fp4_ctas(const AttendFp4Params &p, int ne) {
+  const int sms = num_sms(), budget = p.max_ctas > 0 && p.max_ctas < sms ? p.max_ctas : sms;
+  const int nw = std::min(p.w, p.max_pos + 1);
+  const long long tiles = (long long)p.B * ((nw + KT - 1) / KT + (ne + KT - 1) / KT);
+  return (int)std::max<long long>(1, std::min<long long>(budget, tiles));
+}
+size_t fp4_align(size_t n) { return (n + 255) & ~(size_t)255; }
+
+template <int C>
+int launch_fp4(const AttendFp4Params &p, const Fp4Plan &pl, cudaStream_t s) {
+  static std::atomic<bool> attr_dev[kMaxDevices];
+  std::atomic<bool> &attr = attr_dev[device_slot()];
+  if (!attr) {
+    const cudaError_t e = cudaFuncSetAttribute(attend_fp4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)Fp4Layout<C>::bytes);
+    if (e != cudaSuccess) return fail(HCA_ERR_CUDA, "attend_fp4 smem attribute: %s", cudaGetErrorString(e));
+    attr = true;
+  }
+  return HCA_LAUNCH("attend_fp4", s, attend_fp4_kernel<C><<<pl.G, kThreads, Fp4Layout<C>::bytes, s>>>(p, pl));
 }
 
 }  // namespace
 
-size_t attend_fp4_workspace_bytes(const AttendFp4Params &) { return 0; }
+// One CTA finishes every sequence itself and needs no workspace.
+size_t attend_fp4_workspace_bytes(const AttendFp4Params &p) {
+  const size_t G = (size_t)fp4_ctas(p, std::max(p.k, (p.max_pos + 1) / p.m));   // listed or not
+  return G == 1 ? 0 : fp4_align(2 * G * p.n_h * p.c * 4) + fp4_align(2 * G * p.n_h * 8) + fp4_align((size_t)p.B * 16);
+}
 
-int run_attend_fp4(const AttendFp4Params &p, void *, size_t, cudaStream_t s) {
-  const size_t smem = ((kSimpleTile + 1) * (size_t)p.c + kSimpleTile) * 4;
-  return HCA_LAUNCH("attend_fp4", s, attend_fp4_simple_kernel<<<dim3(p.n_h, p.B), 256, smem, s>>>(p));
+int run_attend_fp4(const AttendFp4Params &p, void *ws, size_t, cudaStream_t s) {
+  Fp4Plan pl{};
+  pl.G = fp4_ctas(p, p.idx ? p.k : (p.max_pos + 1) / p.m);
+  pl.fd_m = make_fastdiv((uint32_t)p.m);
+  pl.fd_cap = make_fastdiv((uint32_t)std::max(p.cap, 1));
+  if (pl.G > 1) {
+    char *w = static_cast<char *>(ws);
+    pl.part_o = reinterpret_cast<float *>(w);
+    w += fp4_align((size_t)2 * pl.G * p.n_h * p.c * 4);
+    pl.part_ml = reinterpret_cast<float2 *>(w);
+    w += fp4_align((size_t)2 * pl.G * p.n_h * 8);
+    pl.meta = reinterpret_cast<int4 *>(w);
+  }
+  const int rc = p.c == 128 ? launch_fp4<128>(p, pl, s) : p.c == 256 ? launch_fp4<256>(p, pl, s) : launch_fp4<512>(p, pl, s);
+  if (rc || pl.G == 1) return rc;
+  LaunchScope ls("attend_fp4_combine", s);
+  cudaLaunchConfig_t cfg{};
+  const int heads = 512 / p.c;
+  cfg.gridDim = dim3(p.B, (p.n_h + heads - 1) / heads, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp4_combine_kernel, p, pl);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return fail(HCA_ERR_CUDA, "attend_fp4_combine launch: %s", cudaGetErrorString(e));
+  }
+  return ls.done();
 }
 
 }  // namespace hca
