@@ -568,7 +568,8 @@ typedef struct {
  * are skipped; an entry listed twice in idx counts twice.
  * q, o [B, n_h, c] HCA_BF16, n_h <= 64, c in {128, 256, 512}, (c, rd) as in
  * hca_kv_fp4_row_bytes; sink [n_h] fp32, NULL = no sink; kv_mixed must be 0;
- * max_ctas as in hca_attend.  q and KV values must be finite.
+ * max_ctas as in hca_attend; B times the most keys of a sequence below 2^37.
+ * q and KV values must be finite.  o may not overlap an input or ws.
  * ws: scratch of hca_attend_fp4_workspace_size bytes (16-byte aligned), which
  * calls that may overlap in time must not share. */
 size_t hca_attend_fp4_workspace_size(const hca_attn_desc *d, int max_pos);

@@ -14,7 +14,7 @@
 // unnormalised fp32 parts, which fp4_combine_kernel joins in their order.
 //
 // Per tile (tcgen05, the sequence's n_h <= 64 heads as the MMA's M = 64):
-//   8 loader warps   records of a tile one tile ahead in registers, codes to
+//   16 loader warps  records of a tile one tile ahead in registers, codes to
 //                    bf16 (exact: two significant bits and a power of two) in
 //                    a 128B-swizzled shared-memory tile that serves as K
 //                    (K-major) and V (MN-major); skipped keys as zero rows
@@ -38,7 +38,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int KT = 64;
-constexpr int kMmaWarp = 4, kLoad0 = 5, kLoadWarps = 8;
+constexpr int kMmaWarp = 4, kLoad0 = 5, kLoadWarps = 16;
 constexpr int kThreads = (kLoad0 + kLoadWarps) * 32;
 constexpr uint32_t kTileBytes = 64 * 128;   // 64 rows x 128 B: one 64-channel block of a tile
 constexpr int SP = 2;                        // S and P buffers
@@ -82,7 +82,7 @@ struct Fp4Layout {
   static constexpr uint32_t bar_off = p_off + SP * kTileBytes;
   static constexpr uint32_t mask_off = bar_off + 512;            // [NS][2] uint32: keys of a stage
   static constexpr uint32_t run_off = mask_off + 64;             // [8] int: this CTA's run
-  static constexpr uint32_t sum_off = run_off + 64;              // [16] long long: prefix sums
+  static constexpr uint32_t sum_off = run_off + 64;              // [32] int: sums of the warps
   static constexpr uint32_t rope_off = sum_off + 128;            // [256] float2
   static constexpr uint32_t bytes = rope_off + 2048 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory");
@@ -100,18 +100,17 @@ struct Fp4Bars {
 // = tiles of all sequences before the run's first tile.
 struct Fp4Run {
   int b0, j0;
-  long long n, before, base, rem;
+  int n, before, base, rem;
 };
 // Runs are base or base + 1 tiles long, the first rem ones the longer.
-__device__ __forceinline__ int fp4_cta_of(const Fp4Run &r, long long tile) {
-  const long long cut = r.rem * (r.base + 1);
-  return (int)(tile < cut ? tile / (r.base + 1) : r.rem + (tile - cut) / r.base);
+__device__ __forceinline__ int fp4_cta_of(const Fp4Run &r, int tile) {
+  const int cut = r.rem * (r.base + 1);
+  return tile < cut ? tile / (r.base + 1) : r.rem + (tile - cut) / r.base;
 }
 
 // Walks the pieces of a run: tiles [j, j + cnt) of sequence b.
 struct Fp4Walk {
-  int b, j, cnt;
-  long long left;
+  int b, j, cnt, left;
   Fp4Keys k;
 };
 __device__ __forceinline__ Fp4Walk fp4_walk(const Fp4Run &r) {
@@ -130,7 +129,7 @@ __device__ __forceinline__ bool fp4_next(const AttendFp4Params &p, const Fp4Plan
     w.k = fp4_keys(p, pl, w.b);
   } while (w.k.nt == 0);
   w.j = w.b == r.b0 ? r.j0 : 0;
-  w.cnt = (int)min((long long)(w.k.nt - w.j), w.left);
+  w.cnt = min(w.k.nt - w.j, w.left);
   w.left -= w.cnt;
   return true;
 }
@@ -148,9 +147,9 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
                                          Fp4Bars *bars) {
   using L = Fp4Layout<C>;
   const int pt = threadIdx.x - kLoad0 * 32, lw = pt >> 5, lane = pt & 31;
-  const int kk = (lw & 1) * 32 + lane, grp = lw >> 1;          // key of the tile, quarter of the record
+  const int kk = (lw & 1) * 32 + lane, grp = lw >> 1;          // key of the tile, eighth of the record
   const int nq = C - p.rd, units = nq / 32, rch = p.rd / 8;     // 16-byte code units, 16-byte RoPE chunks
-  const int per = units <= 4 ? 1 : units <= 8 ? 2 : 4;          // units of this thread: u0 .. u0 + per - 1
+  const int per = units <= 8 ? 1 : 2;                           // units of this thread: u0 .. u0 + per - 1
   const int u0 = grp * per;
   const int eoff = nq / 2 + 2 * p.rd;
   const uint32_t sbase = smem_u32(smem);
@@ -186,38 +185,39 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
     const int pi = fdiv(x.e, pl.fd_cap), pg = __ldg(p.pages + (long long)x.b * p.max_pages + pi);
     return pg >= 0 && pg < p.n_pages ? (long long)pg * p.cap + (x.e - pi * p.cap) : -1;
   };
-  struct Data {
-    uint4 c[4], r[2];
-    uint32_t e;
+  // what this thread holds of the next tile's record; each part is loaded again
+  // as soon as it has been used, a tile's time before its next use
+  uint4 c[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, rc = make_uint4(0, 0, 0, 0);
+  uint32_t ex = 0u;
+  auto load_c = [&](const unsigned char *rp, int i) {
+    c[i] = rp && i < per && u0 + i < units ? __ldg(reinterpret_cast<const uint4 *>(rp) + u0 + i) : make_uint4(0, 0, 0, 0);
   };
-  auto fetch = [&](long long row, Data &d) {
-    const unsigned char *rp = p.rows + row * p.rec;
-    const bool on = row >= 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      d.c[i] = on && i < per && u0 + i < units ? __ldg(reinterpret_cast<const uint4 *>(rp) + u0 + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      d.r[i] = on && grp + 4 * i < rch ? __ldg(reinterpret_cast<const uint4 *>(rp + nq / 2) + grp + 4 * i) : make_uint4(0, 0, 0, 0);
-    d.e = 0u;
-    if (on && u0 < units) {       // u0 is a multiple of per, and the record padded to 16 bytes
-      if (per == 4) d.e = __ldg(reinterpret_cast<const uint32_t *>(rp + eoff + u0));
-      else if (per == 2) d.e = __ldg(reinterpret_cast<const unsigned short *>(rp + eoff + u0));
-      else d.e = __ldg(rp + eoff + u0);
-    }
+  auto load_r = [&](const unsigned char *rp) {
+    rc = rp && grp < rch ? __ldg(reinterpret_cast<const uint4 *>(rp + nq / 2) + grp) : make_uint4(0, 0, 0, 0);
+  };
+  auto load_e = [&](const unsigned char *rp) -> uint32_t {
+    if (!rp || u0 >= units) return 0u;      // u0 is a multiple of per, and the record padded to 16 bytes
+    return per == 2 ? (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(rp + eoff + u0)) : (uint32_t)__ldg(rp + eoff + u0);
+  };
+  auto record = [&](long long row) { return row >= 0 ? p.rows + row * p.rec : nullptr; };
+  // records two tiles ahead are asked into L2: 128 bytes per thread of the first groups
+  auto prefetch = [&](const unsigned char *rp) {
+    if (rp && 128 * grp < p.rec) asm volatile("prefetch.global.L2 [%0];" ::"l"(rp + 128 * grp));
   };
 
   Fp4Tile a, n1, n2;
   bool h0 = next_tile(a), h1 = h0 && next_tile(n1), h2 = h1 && next_tile(n2);
-  long long row0 = h0 ? row_of(a) : -1, row1 = h1 ? row_of(n1) : -1;
-  Data d0, d1;
-  if (h0) fetch(row0, d0);
+  const unsigned char *r0 = h0 ? record(row_of(a)) : nullptr, *r1 = h1 ? record(row_of(n1)) : nullptr;
+  load_c(r0, 0);
+  load_c(r0, 1);
+  load_r(r0);
+  ex = load_e(r0);
   int st = 0;
   uint32_t ph = 1;
   while (h0) {
-    // one tile ahead its records, two its rows, three its entries
-    if (h1) fetch(row1, d1);
-    const long long row2 = h2 ? row_of(n2) : -1;
+    // one tile ahead records, two rows, three entries
+    const uint32_t exn = load_e(r1);
+    const unsigned char *r2 = h2 ? record(row_of(n2)) : nullptr;
     Fp4Tile n3;
     const bool h3 = h2 && next_tile(n3);
 
@@ -229,7 +229,7 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
       constexpr int CPR = C / 8, RPP = kLoadWarps * 32 / CPR;
       const int chunk = pt % CPR;
       const uint32_t dst = sbase + st * L::NKB * kTileBytes + (chunk / 8) * kTileBytes;
-#pragma unroll 8
+#pragma unroll 4
       for (int r = pt / CPR; r < KT; r += RPP) {
         const bool on = r < a.wcnt;
         const __nv_bfloat16 *src = p.kv_win + ((long long)a.b * p.w + (on ? (a.win0 + r) % p.w : 0)) * C + chunk * 8;
@@ -241,38 +241,44 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
         mask[1] = range_bits(32, 0, a.wcnt);
         mbar_arrive(smem_u32(&bars->kv_full[st]));
       }
+      load_c(r1, 0);
+      load_c(r1, 1);
+      load_r(r1);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const int u = u0 + i;                       // channels 32 u .. 32 u + 31
-        if (i >= per || u >= units) break;
-        const float sc = pow2f(max((int)((d0.e >> (8 * i)) & 255u), 1) - 127);   // byte 0: all codes are zero
-        const uint32_t wd[4] = {d0.c[i].x, d0.c[i].y, d0.c[i].z, d0.c[i].w};
-        uint8_t *dst = tile + (u / 2) * kTileBytes;
+        if (i < per && u < units) {
+          const float sc = pow2f(max((int)((ex >> (8 * i)) & 255u), 1) - 127);   // byte 0: all codes are zero
+          const uint32_t wd[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+          uint8_t *dst = tile + (u / 2) * kTileBytes;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t f[4], o[4];
-          e2m1x8_f16(wd[h], f);
+          for (int h = 0; h < 4; ++h) {
+            uint32_t f[4], o[4];
+            e2m1x8_f16(wd[h], f);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f[q]));
-            o[q] = pack_bf16x2(v.x * sc, v.y * sc);
+            for (int q = 0; q < 4; ++q) {
+              const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f[q]));
+              o[q] = pack_bf16x2(v.x * sc, v.y * sc);
+            }
+            *reinterpret_cast<uint4 *>(dst + sw128_off(kk, (u & 1) * 4 + h)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          *reinterpret_cast<uint4 *>(dst + sw128_off(kk, (u & 1) * 4 + h)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        load_c(r1, i);
       }
-      for (int i = 0, ch = grp; ch < rch; ch += 4, ++i) {
+      for (int ch = grp; ch < rch; ch += 8) {
         const int c8 = nq / 8 + ch;
-        uint4 v = i == 0 ? d0.r[0] : d0.r[1];
-        if (i > 1) v = row0 >= 0 ? __ldg(reinterpret_cast<const uint4 *>(p.rows + row0 * p.rec + nq / 2) + ch) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(tile + (c8 / 8) * kTileBytes + sw128_off(kk, c8 % 8)) = v;
+        if (ch >= 8) rc = r0 ? __ldg(reinterpret_cast<const uint4 *>(r0 + nq / 2) + ch) : make_uint4(0, 0, 0, 0);   // rd > 64
+        *reinterpret_cast<uint4 *>(tile + (c8 / 8) * kTileBytes + sw128_off(kk, c8 % 8)) = rc;
       }
-      const uint32_t m = __ballot_sync(0xffffffffu, row0 >= 0);
+      load_r(r1);
+      const uint32_t m = __ballot_sync(0xffffffffu, r0 != nullptr);
       if (grp == 0 && lane == 0) mask[lw] = m;
       fence_proxy_async();      // the tensor cores read the tile through the async proxy
       mbar_arrive(smem_u32(&bars->kv_full[st]));
       if (pt == 0) mbar_arrive(smem_u32(&bars->kv_full[st]));
     }
+    prefetch(r2);
     if (++st == L::NS) {
       st = 0;
       ph ^= 1;
@@ -280,9 +286,9 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
     a = n1;
     n1 = n2;
     n2 = n3;
-    row0 = row1;
-    row1 = row2;
-    d0 = d1;
+    r0 = r1;
+    r1 = r2;
+    ex = exn;
     h0 = h1;
     h1 = h2;
     h2 = h3;
@@ -381,7 +387,7 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
   uint32_t g = 0;                         // tiles so far
   int ks = 0, npiece = 0;
   uint32_t kph = 0;
-  long long before = run.before;
+  int before = run.before;
 
   for (Fp4Walk w = fp4_walk(run); fp4_next(p, pl, run, w); ++npiece) {
     // ---- Q into tensor memory (the previous piece's last S has been read)
@@ -494,7 +500,7 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
     }
     if (pl.meta && threadIdx.x == 0 && w.j == 0) {
       // the CTA that has a sequence's first tile says who else has some
-      const long long last = before + w.k.nt - 1;
+      const int last = before + w.k.nt - 1;
       pl.meta[w.b] = whole ? make_int4(-1, 0, 0, 0)
                            : make_int4(blockIdx.x, fp4_cta_of(run, last), before == run.before ? 0 : 1, 0);
     }
@@ -503,45 +509,50 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
       if (!mbar_wait_fast(bar(bars->pv_done[gl % SP]), (gl / SP) & 1, p.status)) return;
     }
     tc_fence_after();
-    const long long slot = 2 * blockIdx.x + (before == run.before ? 0 : 1);
+    const long long slot = 2 * (int)blockIdx.x + (before == run.before ? 0 : 1);
     float inv = 0.f;
     if (m_used != -INFINITY) inv = 1.f / (ltot + (p.sink && live ? exp2f(p.sink[r] * kLog2e - m_used) : 0.f));
     if (!whole && live && half == 0) pl.part_ml[slot * p.n_h + r] = make_float2(m_used, ltot);
+    // 32 columns of each half at a time by way of the warp's 4 KB of the P
+    // buffers (free: the last P V has completed), so that whole 128-byte lines
+    // leave; thread-by-thread stores of a row each took 10000 cycles at c = 512
+    uint8_t *stage = smem + L::p_off + warp * 4096;          // [16 rows][2 halves][32 columns] fp32, chunks swizzled by row
 #pragma unroll 1
-    for (int c0 = 0; c0 < C / 2; c0 += 16) {
-      uint32_t ov[16];
-      tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0, ov);
+    for (int c0 = 0; c0 < C / 2; c0 += 32) {
+      uint32_t ov[32];
+      tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&ov[0]));
+      tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&ov[16]));
       tmem_ld_wait();
-      if (!live) continue;
-      const int col0 = half * (C / 2) + c0;
-      if (!whole) {
-        float4 *dst = reinterpret_cast<float4 *>(pl.part_o + (slot * p.n_h + r) * C + col0);
+      __syncwarp();                                          // the step before has been read
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          dst[x] = make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]),
-                               __uint_as_float(ov[4 * x + 3]));
-        continue;
-      }
-      float v[16];
+      for (int x = 0; x < 8; ++x)
+        *reinterpret_cast<uint4 *>(stage + hl * 256 + half * 128 + ((x ^ (hl & 7)) << 4)) =
+            make_uint4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
+      __syncwarp();
+      // lanes 8 i .. 8 i + 7: the 32 columns of one (row, half)
+      const int x = lane & 7;
 #pragma unroll
-      for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(ov[x]) * inv;
-      if (col0 >= C - p.rd) {             // rd is a multiple of 64
-        const float2 *t = rope + (col0 - (C - p.rd)) / 2;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const float2 cs = t[x];
-          const float a = v[2 * x], b = v[2 * x + 1];
-          v[2 * x] = a * cs.x + b * cs.y;
-          v[2 * x + 1] = b * cs.x - a * cs.y;
+      for (int i = 0; i < 8; ++i) {
+        const int rh = 4 * i + (lane >> 3), row = rh >> 1, hf = rh & 1, head = warp * 16 + row;
+        const float4 v = *reinterpret_cast<const float4 *>(stage + row * 256 + hf * 128 + ((x ^ (row & 7)) << 4));
+        const float iv = __shfl_sync(0xffffffffu, inv, row);
+        if (head >= p.n_h) continue;
+        const int col = hf * (C / 2) + c0 + 4 * x;
+        if (!whole) {
+          *reinterpret_cast<float4 *>(pl.part_o + (slot * p.n_h + head) * C + col) = v;
+          continue;
         }
+        float4 y = make_float4(v.x * iv, v.y * iv, v.z * iv, v.w * iv);
+        if (col >= C - p.rd) {
+          const float2 *t = rope + (col - (C - p.rd)) / 2;
+          const float2 s0 = t[0], s1 = t[1];
+          y = make_float4(y.x * s0.x + y.y * s0.y, y.y * s0.x - y.x * s0.y, y.z * s1.x + y.w * s1.y, y.w * s1.x - y.z * s1.y);
+        }
+        *reinterpret_cast<uint2 *>(p.o + ((long long)w.b * p.n_h + head) * C + col) =
+            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
       }
-      uint32_t o[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) o[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
-      uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((long long)w.b * p.n_h + r) * C + col0);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    fence_proxy_async();                                     // P is written there next
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(bars->o_empty));
@@ -579,46 +590,41 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
   }
   pdl_trigger();
   // ---- this CTA's run: tiles of all sequences summed up, then the sequence where the run begins
-  long long *sums = reinterpret_cast<long long *>(smem + L::sum_off);
+  int *sums = reinterpret_cast<int *>(smem + L::sum_off);
   Fp4Run run;
   {
-    long long mine = 0;
+    constexpr int NW = kThreads / 32;
+    int mine = 0;
     for (int b = threadIdx.x; b < p.B; b += kThreads) mine += fp4_keys(p, pl, b).nt;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    mine = __reduce_add_sync(0xffffffffu, mine);
     if (lane == 0) sums[warp] = mine;
     __syncthreads();
-    long long total = 0;
-    for (int i = 0; i < kThreads / 32; ++i) total += sums[i];
+    const int total = __reduce_add_sync(0xffffffffu, lane < NW ? sums[lane] : 0);
     run.base = total / pl.G;
     run.rem = total - run.base * pl.G;
-    run.before = blockIdx.x * run.base + min((long long)blockIdx.x, run.rem);
-    run.n = run.base + (blockIdx.x < run.rem ? 1 : 0);
+    run.before = blockIdx.x * run.base + min((int)blockIdx.x, run.rem);
+    run.n = run.base + ((int)blockIdx.x < run.rem ? 1 : 0);
     int *at = reinterpret_cast<int *>(smem + L::run_off);
-    long long done = 0;
+    int done = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
       const int nt = b < p.B ? fp4_keys(p, pl, b).nt : 0;
-      long long x = nt;                   // inclusive scan over the warp
+      int x = nt;                         // inclusive scan over the warp, then over the warps
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
       __syncthreads();
       if (lane == 31) sums[warp] = x;
       __syncthreads();
-      long long all = 0;
-      for (int i = 0; i < kThreads / 32; ++i) {
-        if (i == warp) x += all;
-        all += sums[i];
-      }
-      const long long first = done + x - nt;
+      const int t = lane < NW ? sums[lane] : 0;
+      const int first = done + __reduce_add_sync(0xffffffffu, lane < warp ? t : 0) + x - nt;
       if (nt > 0 && run.before >= first && run.before < first + nt) {
         at[0] = b;
-        at[1] = (int)(run.before - first);
+        at[1] = run.before - first;
       }
-      done += all;
+      done += __reduce_add_sync(0xffffffffu, t);
     }
     tc_fence_before();
     __syncthreads();

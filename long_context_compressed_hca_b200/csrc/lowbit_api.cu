@@ -1,5 +1,6 @@
 // lowbit_api.cu -- the extern "C" entry points of the low-bit decode step:
 // host-side validation and dispatch.  See include/hca.h.
+#include <algorithm>
 #include <climits>
 
 #include "internal.h"
@@ -189,6 +190,8 @@ static int attend_fp4_params(const hca_attn_desc *d, int max_pos, AttendFp4Param
   REQUIRE(d->max_ctas >= 0, "max_ctas must be >= 0 (0 = every SM)");
   REQUIRE(max_pos >= 0 && max_pos <= INT_MAX - 4096, "max_pos must be in [0, 2^31 - 4096)");
   REQUIRE(d->w <= (1 << 20) && d->k <= (1 << 28), "w must be <= 2^20 and k <= 2^28");
+  const long long most = std::max<long long>(d->k, ((long long)max_pos + 1) / d->m);
+  REQUIRE((long long)d->B * (d->w / 64 + most / 64 + 2) <= INT_MAX, "B times the keys of a sequence must be below 2^37");
   *p = AttendFp4Params{};
   p->B = d->B; p->n_h = d->n_h; p->c = d->c; p->rd = d->rd; p->w = d->w; p->m = d->m; p->k = d->k;
   p->rec = (int)kv_fp4_row_bytes(d->c, d->rd);
