@@ -6,7 +6,7 @@
 // are visible); z_j = scale q_h . row_j; o_h = sum_j e^{z_j} row_j /
 // (sum_j e^{z_j} + e^{sink_h}); the last rd dims of o_h rotated by -pos.
 //
-// Keys are taken 64 at a time, a sequence's window tiles first.  The tiles of
+// Keys are taken 64 at a time, a sequence's window tiles last.  The tiles of
 // all sequences form one list, and every CTA takes an equal run of it, so that
 // ragged lengths cost nothing and few sequences still fill the GPU; the runs
 // follow from the positions on the device, which each CTA sums up itself.  A
@@ -14,10 +14,12 @@
 // unnormalised fp32 parts, which fp4_combine_kernel joins in their order.
 //
 // Per tile (tcgen05, the sequence's n_h <= 64 heads as the MMA's M = 64):
-//   16 loader warps  records of a tile one tile ahead in registers, codes to
-//                    bf16 (exact: two significant bits and a power of two) in
-//                    a 128B-swizzled shared-memory tile that serves as K
-//                    (K-major) and V (MN-major); skipped keys as zero rows
+//   8 loader warps   codes of the next tile on their way into shared memory
+//                    (cp.async, every thread its own parts: no barrier) while
+//                    this one's become bf16 (exact: two significant bits and a
+//                    power of two) in a 128B-swizzled tile that serves as K
+//                    (K-major) and V (MN-major); RoPE channels and window rows
+//                    are copied into the tile, skipped keys are zero rows
 //   1 MMA warp       S = Q K^T (Q in tensor memory, the A operand), O += P V;
 //                    S of the next tile is issued before P V of this one
 //   4 softmax warps  S from tensor memory, running maximum moved only when it
@@ -38,7 +40,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int KT = 64;
-constexpr int kMmaWarp = 4, kLoad0 = 5, kLoadWarps = 16;
+constexpr int kMmaWarp = 4, kLoad0 = 5, kLoadWarps = 8;
 constexpr int kThreads = (kLoad0 + kLoadWarps) * 32;
 constexpr uint32_t kTileBytes = 64 * 128;   // 64 rows x 128 B: one 64-channel block of a tile
 constexpr int SP = 2;                        // S and P buffers
@@ -47,10 +49,17 @@ constexpr int SP = 2;                        // S and P buffers
 struct Fp4Plan {
   int G;                   // CTAs
   FastDiv fd_m, fd_cap;
-  float *part_o;           // [2 G][n_h][c]
+  float4 *part_o;          // [2 G] parts of fp4_part's layout
   float2 *part_ml;         // [2 G][n_h]
   int4 *meta;              // [B]: first and last CTA of a cut sequence and the first one's slot; x < 0: finished
 };
+
+// A part's O: for every 16 heads and 4 columns i, i + 1, .. of either half of
+// the channels, the 32 threads (half, head) side by side.  float4 index of
+// heads 16 q .. and columns 4 i of part `slot`, thread 0.
+__device__ __forceinline__ long long fp4_part(const AttendFp4Params &p, long long slot, int q, int i) {
+  return ((slot * ((p.n_h + 15) / 16) + q) * (p.c / 8) + i) * 32;
+}
 
 // The key set of sequence b.
 struct Fp4Keys {
@@ -77,14 +86,15 @@ __device__ __forceinline__ Fp4Keys fp4_keys(const AttendFp4Params &p, const Fp4P
 template <int C>
 struct Fp4Layout {
   static constexpr int NKB = C / 64;
-  static constexpr int NS = C == 512 ? 3 : C == 256 ? 6 : 8;    // key-tile stages
+  static constexpr int NS = C == 512 ? 3 : C == 256 ? 6 : 8;     // key-tile stages
+  static constexpr uint32_t kRawBytes = 256 * (4 * 16 + 4);      // a tile's codes: 4 chunks and 4 exponents per thread
   static constexpr uint32_t p_off = NS * NKB * kTileBytes;
-  static constexpr uint32_t bar_off = p_off + SP * kTileBytes;
+  static constexpr uint32_t raw_off = p_off + SP * kTileBytes;
+  static constexpr uint32_t bar_off = raw_off + kRawBytes;
   static constexpr uint32_t mask_off = bar_off + 512;            // [NS][2] uint32: keys of a stage
   static constexpr uint32_t run_off = mask_off + 64;             // [8] int: this CTA's run
   static constexpr uint32_t sum_off = run_off + 64;              // [32] int: sums of the warps
-  static constexpr uint32_t rope_off = sum_off + 128;            // [256] float2
-  static constexpr uint32_t bytes = rope_off + 2048 + 1024;
+  static constexpr uint32_t bytes = sum_off + 128 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory");
   // tensor memory: O in lane-half 0, columns [0, C); in lane-half 1 S buffers
   // at [0, 128) and Q (bf16, two per column) at [128, 128 + C / 2)
@@ -135,11 +145,15 @@ __device__ __forceinline__ bool fp4_next(const AttendFp4Params &p, const Fp4Plan
 }
 
 // ---------------------------------------------------------------- loaders
-// Where the loader threads find a tile: thread (key, group) of an entry tile
-// its record (row < 0: skipped), of a window tile the first token.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
+// A tile on its way through a loader thread (one of 4 for one of 64 keys).
 struct Fp4Tile {
-  int b, win0, wcnt;       // window tile: sequence, first token, rows; win0 < 0: entry tile
-  int e;                   // entry of this thread's key, -1: none
+  int kind;                // 0: none, 1: entries, 2: window rows
+  int b, e, win0;          // sequence; entry of this thread's key; first token of the rows
+  int cnt;                 // visible entries, then whether the key has a record; rows of a window tile
 };
 
 template <int C>
@@ -147,151 +161,135 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
                                          Fp4Bars *bars) {
   using L = Fp4Layout<C>;
   const int pt = threadIdx.x - kLoad0 * 32, lw = pt >> 5, lane = pt & 31;
-  const int kk = (lw & 1) * 32 + lane, grp = lw >> 1;          // key of the tile, eighth of the record
+  const int kk = (lw & 1) * 32 + lane, grp = lw >> 1;          // key of the tile, quarter of the record
   const int nq = C - p.rd, units = nq / 32, rch = p.rd / 8;     // 16-byte code units, 16-byte RoPE chunks
-  const int per = units <= 8 ? 1 : 2;                           // units of this thread: u0 .. u0 + per - 1
-  const int u0 = grp * per;
-  const int eoff = nq / 2 + 2 * p.rd;
-  const uint32_t sbase = smem_u32(smem);
+  const int per = units <= 4 ? 1 : units <= 8 ? 2 : 4;          // units of this thread: u0 .. u0 + nu - 1
+  const int u0 = grp * per, nu = max(0, min(per, units - u0));
+  const int eoff = nq / 2 + 2 * p.rd + (u0 & ~3), esh = 8 * (u0 & 3);
+  const uint32_t sbase = smem_u32(smem), rawc = sbase + L::raw_off + pt * 16, rawe = sbase + L::raw_off + 4 * 4096 + pt * 4;
+  const unsigned char *none = reinterpret_cast<const unsigned char *>(p.q);   // an address for copies of nothing
 
   Fp4Walk w = fp4_walk(run);
   int t = 0;                                                     // next tile of the piece
-  // tile descriptors in order; the entry index (a load) is resolved as early as possible
-  auto next_tile = [&](Fp4Tile &x) -> bool {
-    if (t == w.cnt) {
-      if (!fp4_next(p, pl, run, w)) return false;
+  bool more = true;
+  // The loads of a tile stand in three rounds of one loop -- its entries, their
+  // pages, their codes -- so that none is waited for in the round that issues
+  // it: t3 entry on its way, t2 page on its way, t1 codes asked for, t0 written
+  // to its stage.
+  Fp4Tile t0{}, t1{}, t2{}, t3{};
+  const unsigned char *rp0 = none, *rp1 = none;
+  int pg = 0, st = 0;
+  uint32_t ph = 1;
+  while (true) {
+    // ---- codes' address of t1 from the page that the round before asked for
+    rp1 = none;
+    if (t1.kind == 1 && t1.cnt) {
+      long long row = (long long)t1.b * p.cap + t1.e;
+      if (p.pages) {
+        t1.cnt = pg >= 0 && pg < p.n_pages;
+        row = (long long)pg * p.cap + (t1.e - fdiv(t1.e, pl.fd_cap) * p.cap);
+      }
+      if (t1.cnt) rp1 = p.rows + row * p.rec;
+    }
+    // ---- page of t2
+    if (t2.kind == 1) {
+      t2.cnt = t2.e >= 0 && t2.e < t2.cnt;
+      if (p.pages && t2.cnt) pg = __ldg(p.pages + (long long)t2.b * p.max_pages + fdiv(t2.e, pl.fd_cap));
+    }
+    // ---- the next tile
+    t3.kind = 0;
+    if (more && t == w.cnt) {
+      more = fp4_next(p, pl, run, w);
       t = 0;
     }
-    const int j = w.j + t++;
-    x.b = w.b;
-    x.win0 = -1;
-    x.e = -1;
-    if (j < w.k.nwt) {
-      x.win0 = w.k.pos - w.k.nw + 1 + j * KT;
-      x.wcnt = min(KT, w.k.nw - j * KT);
-    } else {
-      const int s = (j - w.k.nwt) * KT + kk;
-      if (s < w.k.ne) {
-        x.e = p.idx ? __ldg(p.idx + (long long)w.b * p.k + s) : s;
-        if (x.e >= w.k.V) x.e = -1;
+    if (more) {
+      const int j = w.j + t++, net = w.k.nt - w.k.nwt;
+      t3.b = w.b;
+      if (j < net) {
+        t3.kind = 1;
+        t3.cnt = w.k.V;
+        t3.e = j * KT + kk;
+        if (p.idx) t3.e = t3.e < w.k.ne ? __ldg(p.idx + (long long)w.b * p.k + t3.e) : -1;
+      } else {
+        t3.kind = 2;
+        t3.win0 = w.k.pos - w.k.nw + 1 + (j - net) * KT;
+        t3.cnt = min(KT, w.k.nw - (j - net) * KT);
       }
     }
-    return true;
-  };
-  // record of the tile's key: index of its row, -1 = skipped
-  auto row_of = [&](const Fp4Tile &x) -> long long {
-    if (x.win0 >= 0 || x.e < 0) return -1;
-    if (!p.pages) return (long long)x.b * p.cap + x.e;
-    const int pi = fdiv(x.e, pl.fd_cap), pg = __ldg(p.pages + (long long)x.b * p.max_pages + pi);
-    return pg >= 0 && pg < p.n_pages ? (long long)pg * p.cap + (x.e - pi * p.cap) : -1;
-  };
-  // what this thread holds of the next tile's record; each part is loaded again
-  // as soon as it has been used, a tile's time before its next use
-  uint4 c[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, rc = make_uint4(0, 0, 0, 0);
-  uint32_t ex = 0u;
-  auto load_c = [&](const unsigned char *rp, int i) {
-    c[i] = rp && i < per && u0 + i < units ? __ldg(reinterpret_cast<const uint4 *>(rp) + u0 + i) : make_uint4(0, 0, 0, 0);
-  };
-  auto load_r = [&](const unsigned char *rp) {
-    rc = rp && grp < rch ? __ldg(reinterpret_cast<const uint4 *>(rp + nq / 2) + grp) : make_uint4(0, 0, 0, 0);
-  };
-  auto load_e = [&](const unsigned char *rp) -> uint32_t {
-    if (!rp || u0 >= units) return 0u;      // u0 is a multiple of per, and the record padded to 16 bytes
-    return per == 2 ? (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(rp + eoff + u0)) : (uint32_t)__ldg(rp + eoff + u0);
-  };
-  auto record = [&](long long row) { return row >= 0 ? p.rows + row * p.rec : nullptr; };
-  // records two tiles ahead are asked into L2: 128 bytes per thread of the first groups
-  auto prefetch = [&](const unsigned char *rp) {
-    if (rp && 128 * grp < p.rec) asm volatile("prefetch.global.L2 [%0];" ::"l"(rp + 128 * grp));
-  };
-
-  Fp4Tile a, n1, n2;
-  bool h0 = next_tile(a), h1 = h0 && next_tile(n1), h2 = h1 && next_tile(n2);
-  const unsigned char *r0 = h0 ? record(row_of(a)) : nullptr, *r1 = h1 ? record(row_of(n1)) : nullptr;
-  load_c(r0, 0);
-  load_c(r0, 1);
-  load_r(r0);
-  ex = load_e(r0);
-  int st = 0;
-  uint32_t ph = 1;
-  while (h0) {
-    // one tile ahead records, two rows, three entries
-    const uint32_t exn = load_e(r1);
-    const unsigned char *r2 = h2 ? record(row_of(n2)) : nullptr;
-    Fp4Tile n3;
-    const bool h3 = h2 && next_tile(n3);
-
-    if (!mbar_wait_fast(smem_u32(&bars->kv_empty[st]), ph, p.status)) break;
+    if (!(t0.kind | t1.kind | t2.kind | t3.kind)) break;
+    // ---- t0 into its stage
     uint8_t *tile = smem + st * L::NKB * kTileBytes;
-    uint32_t *mask = reinterpret_cast<uint32_t *>(smem + L::mask_off) + 2 * st;
-    if (a.win0 >= 0) {
-      // window rows, 16-byte chunks in the order of the row
-      constexpr int CPR = C / 8, RPP = kLoadWarps * 32 / CPR;
-      const int chunk = pt % CPR;
-      const uint32_t dst = sbase + st * L::NKB * kTileBytes + (chunk / 8) * kTileBytes;
+    const uint32_t full = smem_u32(&bars->kv_full[st]);
+    uint32_t ex = 0u;
+    if (t0.kind) {
+      if (!mbar_wait_fast(smem_u32(&bars->kv_empty[st]), ph, p.status)) break;
+      uint32_t *mask = reinterpret_cast<uint32_t *>(smem + L::mask_off) + 2 * st;
+      const uint32_t tdst = sbase + st * L::NKB * kTileBytes;
+      if (t0.kind == 2) {
+        // window rows, 16-byte chunks in the order of the row
+        constexpr int CPR = C / 8, RPP = kLoadWarps * 32 / CPR;
+        const int chunk = pt % CPR;
+        const __nv_bfloat16 *ring = p.kv_win + (long long)t0.b * p.w * C + chunk * 8;
+        int slot = (t0.win0 + pt / CPR) % p.w;
 #pragma unroll 4
-      for (int r = pt / CPR; r < KT; r += RPP) {
-        const bool on = r < a.wcnt;
-        const __nv_bfloat16 *src = p.kv_win + ((long long)a.b * p.w + (on ? (a.win0 + r) % p.w : 0)) * C + chunk * 8;
-        cp_async16(dst + sw128_off(r, chunk % 8), src, on ? 16 : 0);
-      }
-      cp_async_arrive_noinc(smem_u32(&bars->kv_full[st]));
-      if (pt == 0) {
-        mask[0] = range_bits(0, 0, a.wcnt);
-        mask[1] = range_bits(32, 0, a.wcnt);
-        mbar_arrive(smem_u32(&bars->kv_full[st]));
-      }
-      load_c(r1, 0);
-      load_c(r1, 1);
-      load_r(r1);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int u = u0 + i;                       // channels 32 u .. 32 u + 31
-        if (i < per && u < units) {
-          const float sc = pow2f(max((int)((ex >> (8 * i)) & 255u), 1) - 127);   // byte 0: all codes are zero
-          const uint32_t wd[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-          uint8_t *dst = tile + (u / 2) * kTileBytes;
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t f[4], o[4];
-            e2m1x8_f16(wd[h], f);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f[q]));
-              o[q] = pack_bf16x2(v.x * sc, v.y * sc);
-            }
-            *reinterpret_cast<uint4 *>(dst + sw128_off(kk, (u & 1) * 4 + h)) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
+        for (int r = pt / CPR; r < KT; r += RPP) {
+          const bool on = r < t0.cnt;
+          cp_async16(tdst + (chunk / 8) * kTileBytes + sw128_off(r, chunk % 8), ring + (on ? (long long)slot * C : 0), on ? 16 : 0);
+          slot += RPP;
+          while (slot >= p.w) slot -= p.w;
         }
-        load_c(r1, i);
+        if (pt == 0) {
+          mask[0] = range_bits(0, 0, t0.cnt);
+          mask[1] = range_bits(32, 0, t0.cnt);
+        }
+      } else {
+        cp_async_wait_all();               // this thread's codes are here
+        for (int ch = grp; ch < rch; ch += 4)
+          cp_async16(tdst + ((nq / 8 + ch) / 8) * kTileBytes + sw128_off(kk, (nq / 8 + ch) % 8),
+                     rp0 + (t0.cnt ? nq / 2 + 16 * ch : 0), t0.cnt ? 16 : 0);
+        const uint32_t m = __ballot_sync(0xffffffffu, t0.cnt);
+        if (grp == 0 && lane == 0) mask[lw] = m;
+        if (nu) ex = *reinterpret_cast<const uint32_t *>(smem + L::raw_off + 4 * 4096 + pt * 4) >> esh;
       }
-      for (int ch = grp; ch < rch; ch += 8) {
-        const int c8 = nq / 8 + ch;
-        if (ch >= 8) rc = r0 ? __ldg(reinterpret_cast<const uint4 *>(r0 + nq / 2) + ch) : make_uint4(0, 0, 0, 0);   // rd > 64
-        *reinterpret_cast<uint4 *>(tile + (c8 / 8) * kTileBytes + sw128_off(kk, c8 % 8)) = rc;
+      cp_async_arrive_noinc(full);         // before the next tile's copies
+    }
+    // ---- its codes, and in their place those of t1
+    if (nu && t1.kind == 1) cp_async4(rawe, rp1 + (t1.cnt ? eoff : 0), t1.cnt ? 4 : 0);
+#pragma unroll 1
+    for (int i = 0; i < nu; ++i, ex >>= 8) {
+      uint4 c = make_uint4(0, 0, 0, 0);
+      if (t0.kind == 1) c = *reinterpret_cast<const uint4 *>(smem + L::raw_off + i * 4096 + pt * 16);
+      if (t1.kind == 1) cp_async16(rawc + i * 4096, rp1 + (t1.cnt ? 16 * (u0 + i) : 0), t1.cnt ? 16 : 0);
+      if (t0.kind != 1) continue;
+      const int u = u0 + i;                // channels 32 u .. 32 u + 31
+      const float sc = pow2f(max((int)(ex & 255u), 1) - 127);   // byte 0: all codes are zero
+      const uint32_t wd[4] = {c.x, c.y, c.z, c.w};
+      uint8_t *dst = tile + (u / 2) * kTileBytes;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t f[4], o[4];
+        e2m1x8_f16(wd[h], f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f[q]));
+          o[q] = pack_bf16x2(v.x * sc, v.y * sc);
+        }
+        *reinterpret_cast<uint4 *>(dst + sw128_off(kk, (u & 1) * 4 + h)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      load_r(r1);
-      const uint32_t m = __ballot_sync(0xffffffffu, r0 != nullptr);
-      if (grp == 0 && lane == 0) mask[lw] = m;
+    }
+    if (t0.kind) {
       fence_proxy_async();      // the tensor cores read the tile through the async proxy
-      mbar_arrive(smem_u32(&bars->kv_full[st]));
-      if (pt == 0) mbar_arrive(smem_u32(&bars->kv_full[st]));
+      mbar_arrive(full);
+      if (pt == 0) mbar_arrive(full);
+      if (++st == L::NS) {
+        st = 0;
+        ph ^= 1;
+      }
     }
-    prefetch(r2);
-    if (++st == L::NS) {
-      st = 0;
-      ph ^= 1;
-    }
-    a = n1;
-    n1 = n2;
-    n2 = n3;
-    r0 = r1;
-    r1 = r2;
-    ex = exn;
-    h0 = h1;
-    h1 = h2;
-    h2 = h3;
+    t0 = t1;
+    t1 = t2;
+    t2 = t3;
+    rp0 = rp1;
   }
   cp_async_wait_all();
 }
@@ -382,7 +380,7 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
   const bool live = r < p.n_h;
   const float zs = p.scale * kLog2e;
   const uint32_t lane_S = (uint32_t)(warp * 32 + 16) << 16, lane_O = (uint32_t)(warp * 32) << 16;
-  float2 *rope = reinterpret_cast<float2 *>(smem + L::rope_off);
+  float2 *rope = reinterpret_cast<float2 *>(smem + L::p_off);   // [256], between pieces
   auto bar = [&](uint64_t &b) { return smem_u32(&b); };
   uint32_t g = 0;                         // tiles so far
   int ks = 0, npiece = 0;
@@ -489,15 +487,6 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
     // ---- epilogue
     const bool whole = w.cnt == w.k.nt;
     const float ltot = l + __shfl_xor_sync(0xffffffffu, l, 16);
-    if (whole) {
-      asm volatile("bar.sync 1, 128;" ::: "memory");       // the previous table has been read
-      for (int i = threadIdx.x; i < p.rd / 2; i += 128) {
-        float sn, cs;
-        fp4_rope(p, w.k.pos, i, sn, cs);
-        rope[i] = make_float2(cs, sn);
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-    }
     if (pl.meta && threadIdx.x == 0 && w.j == 0) {
       // the CTA that has a sequence's first tile says who else has some
       const int last = before + w.k.nt - 1;
@@ -509,50 +498,66 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
       if (!mbar_wait_fast(bar(bars->pv_done[gl % SP]), (gl / SP) & 1, p.status)) return;
     }
     tc_fence_after();
+    if (whole) {
+      // the rotation's table, where P was: the last P V has completed
+      for (int i = threadIdx.x; i < p.rd / 2; i += 128) {
+        float sn, cs;
+        fp4_rope(p, w.k.pos, i, sn, cs);
+        rope[i] = make_float2(cs, sn);
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
     const long long slot = 2 * (int)blockIdx.x + (before == run.before ? 0 : 1);
     float inv = 0.f;
     if (m_used != -INFINITY) inv = 1.f / (ltot + (p.sink && live ? exp2f(p.sink[r] * kLog2e - m_used) : 0.f));
-    if (!whole && live && half == 0) pl.part_ml[slot * p.n_h + r] = make_float2(m_used, ltot);
-    // 32 columns of each half at a time by way of the warp's 4 KB of the P
-    // buffers (free: the last P V has completed), so that whole 128-byte lines
-    // leave; thread-by-thread stores of a row each took 10000 cycles at c = 512
-    uint8_t *stage = smem + L::p_off + warp * 4096;          // [16 rows][2 halves][32 columns] fp32, chunks swizzled by row
+    if (!whole) {
+      // 16 rows of a warp side by side, so that a store is 512 contiguous bytes
+      if (live && half == 0) pl.part_ml[slot * p.n_h + r] = make_float2(m_used, ltot);
+      if (warp * 16 < p.n_h) {
+        float4 *dst = pl.part_o + fp4_part(p, slot, warp, 0) + lane;
 #pragma unroll 1
-    for (int c0 = 0; c0 < C / 2; c0 += 32) {
-      uint32_t ov[32];
-      tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&ov[0]));
-      tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&ov[16]));
-      tmem_ld_wait();
-      __syncwarp();                                          // the step before has been read
+        for (int c0 = 0; c0 < C / 2; c0 += 32, dst += 256) {
+          uint32_t ov[32];
+          tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&ov[0]));
+          tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&ov[16]));
+          tmem_ld_wait();
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        *reinterpret_cast<uint4 *>(stage + hl * 256 + half * 128 + ((x ^ (hl & 7)) << 4)) =
-            make_uint4(ov[4 * x], ov[4 * x + 1], ov[4 * x + 2], ov[4 * x + 3]);
-      __syncwarp();
-      // lanes 8 i .. 8 i + 7: the 32 columns of one (row, half)
-      const int x = lane & 7;
+          for (int x = 0; x < 8; ++x)
+            dst[32 * x] = make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]),
+                                      __uint_as_float(ov[4 * x + 3]));
+        }
+      }
+    } else {
+      uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((long long)w.b * p.n_h + r) * C + half * (C / 2));
+#pragma unroll 1
+      for (int c0 = 0; c0 < C / 2; c0 += 16, dst += 2) {
+        uint32_t ov[16];
+        tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0, ov);
+        tmem_ld_wait();
+        float v[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int rh = 4 * i + (lane >> 3), row = rh >> 1, hf = rh & 1, head = warp * 16 + row;
-        const float4 v = *reinterpret_cast<const float4 *>(stage + row * 256 + hf * 128 + ((x ^ (row & 7)) << 4));
-        const float iv = __shfl_sync(0xffffffffu, inv, row);
-        if (head >= p.n_h) continue;
-        const int col = hf * (C / 2) + c0 + 4 * x;
-        if (!whole) {
-          *reinterpret_cast<float4 *>(pl.part_o + (slot * p.n_h + head) * C + col) = v;
-          continue;
+        for (int x = 0; x < 16; ++x) v[x] = __uint_as_float(ov[x]) * inv;
+        const int col0 = half * (C / 2) + c0;
+        if (col0 >= C - p.rd) {             // rd is a multiple of 64
+          const float2 *t = rope + (col0 - (C - p.rd)) / 2;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float2 cs = t[x];
+            const float a = v[2 * x], b = v[2 * x + 1];
+            v[2 * x] = a * cs.x + b * cs.y;
+            v[2 * x + 1] = b * cs.x - a * cs.y;
+          }
         }
-        float4 y = make_float4(v.x * iv, v.y * iv, v.z * iv, v.w * iv);
-        if (col >= C - p.rd) {
-          const float2 *t = rope + (col - (C - p.rd)) / 2;
-          const float2 s0 = t[0], s1 = t[1];
-          y = make_float4(y.x * s0.x + y.y * s0.y, y.y * s0.x - y.x * s0.y, y.z * s1.x + y.w * s1.y, y.w * s1.x - y.z * s1.y);
+        uint32_t o[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) o[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+        if (live) {
+          dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        *reinterpret_cast<uint2 *>(p.o + ((long long)w.b * p.n_h + head) * C + col) =
-            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
       }
     }
-    fence_proxy_async();                                     // P is written there next
+    if (whole) asm volatile("bar.sync 1, 128;" ::: "memory");   // the table has been read
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(bars->o_empty));
@@ -573,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
     mbar_init(bar(bars->q_empty), 1);
     mbar_init(bar(bars->o_empty), 4);
     for (int i = 0; i < L::NS; ++i) {
-      mbar_init(bar(bars->kv_full[i]), kLoadWarps * 32 + 1);   // every thread's part of the tile, and the mask
+      mbar_init(bar(bars->kv_full[i]), 2 * kLoadWarps * 32 + 1);   // every thread's copies and stores, and the mask
       mbar_init(bar(bars->kv_empty[i]), 1);
     }
     for (int i = 0; i < SP; ++i) {
@@ -655,38 +660,51 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
 }
 
 // Cut sequences: o = sum_i 2^(m_i - M) O_i / (sum_i 2^(m_i - M) l_i +
-// 2^(sink - M)) over the parts in their order, rotated.  A thread has 4
-// channels of a head; a block 512 / c heads.
+// 2^(sink - M)) over the parts in their order, rotated.  A block has 16 heads
+// and 16 columns of either half, a thread 4 of them.
 __global__ void __launch_bounds__(128) fp4_combine_kernel(AttendFp4Params p, Fp4Plan pl) {
-  const int per = p.c / 4, b = blockIdx.x, h = blockIdx.y * (128 / per) + threadIdx.x / per;
-  const int col = 4 * (threadIdx.x % per);
+  const int lane = threadIdx.x & 31, i = blockIdx.y * 4 + (threadIdx.x >> 5), q = blockIdx.z, b = blockIdx.x;
+  const int h = 16 * q + (lane & 15), col = (lane >> 4) * (p.c / 2) + 4 * i;
   pdl_wait();
   const int4 meta = pl.meta[b];
   if (meta.x < 0 || h >= p.n_h) return;
   const float sink = p.sink ? p.sink[h] * kLog2e : -INFINITY;
-  auto slot = [&](int c) { return (long long)(2 * c + (c == meta.x ? meta.z : 0)) * p.n_h + h; };
-  float M = sink;
-#pragma unroll 4
-  for (int c = meta.x; c <= meta.y; ++c) M = fmaxf(M, pl.part_ml[slot(c)].x);
+  auto slot = [&](int c) { return (long long)(2 * c + (c == meta.x ? meta.z : 0)); };
+  // one pass with a running maximum, 4 parts at a time
+  float M = sink, den = sink == -INFINITY ? 0.f : 1.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (M != -INFINITY) {
-    float den = exp2f(sink - M);
-#pragma unroll 4
-    for (int c = meta.x; c <= meta.y; ++c) {
-      const float2 ml = pl.part_ml[slot(c)];
-      const float4 o = *reinterpret_cast<const float4 *>(pl.part_o + slot(c) * p.c + col);
-      const float f = exp2f(ml.x - M);    // 0 for a part without keys
-      den += f * ml.y;
-      acc.x += f * o.x; acc.y += f * o.y; acc.z += f * o.z; acc.w += f * o.w;
+  for (int c0 = meta.x; c0 <= meta.y; c0 += 4) {
+    float2 ml[4];
+    float4 o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (c0 + k <= meta.y) {
+        ml[k] = pl.part_ml[slot(c0 + k) * p.n_h + h];
+        o[k] = pl.part_o[fp4_part(p, slot(c0 + k), q, i) + lane];
+      }
     }
-    const float inv = 1.f / den;
-    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
+    const float m = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+    if (m == -INFINITY) continue;
+    const float f = exp2f(M - m);
+    M = m;
+    den *= f;
+    acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (ml[k].x == -INFINITY) continue;     // a part without keys
+      const float e = exp2f(ml[k].x - M);
+      den += e * ml[k].y;
+      acc.x += e * o[k].x; acc.y += e * o[k].y; acc.z += e * o[k].z; acc.w += e * o[k].w;
+    }
   }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
   if (col >= p.c - p.rd) {
-    const int pos = min(__ldg(p.positions + b), p.max_pos), i = (col - (p.c - p.rd)) / 2;
+    const int pos = min(__ldg(p.positions + b), p.max_pos), k = (col - (p.c - p.rd)) / 2;
     float s0, c0, s1, c1;
-    fp4_rope(p, pos, i, s0, c0);
-    fp4_rope(p, pos, i + 1, s1, c1);
+    fp4_rope(p, pos, k, s0, c0);
+    fp4_rope(p, pos, k + 1, s1, c1);
     acc = make_float4(acc.x * c0 + acc.y * s0, acc.y * c0 - acc.x * s0, acc.z * c1 + acc.w * s1, acc.w * c1 - acc.z * s1);
   }
   *reinterpret_cast<uint2 *>(p.o + ((long long)b * p.n_h + h) * p.c + col) =
@@ -701,6 +719,7 @@ int fp4_ctas(const AttendFp4Params &p, int ne) {
   return (int)std::max<long long>(1, std::min<long long>(budget, tiles));
 }
 size_t fp4_align(size_t n) { return (n + 255) & ~(size_t)255; }
+size_t fp4_part_bytes(const AttendFp4Params &p, size_t G) { return fp4_align(2 * G * ((p.n_h + 15) / 16 * 16) * p.c * 4); }
 
 template <int C>
 int launch_fp4(const AttendFp4Params &p, const Fp4Plan &pl, cudaStream_t s) {
@@ -720,7 +739,7 @@ int launch_fp4(const AttendFp4Params &p, const Fp4Plan &pl, cudaStream_t s) {
 // One CTA finishes every sequence itself and needs no workspace.
 size_t attend_fp4_workspace_bytes(const AttendFp4Params &p) {
   const size_t G = (size_t)fp4_ctas(p, std::max(p.k, (p.max_pos + 1) / p.m));   // listed or not
-  return G == 1 ? 0 : fp4_align(2 * G * p.n_h * p.c * 4) + fp4_align(2 * G * p.n_h * 8) + fp4_align((size_t)p.B * 16);
+  return G == 1 ? 0 : fp4_part_bytes(p, G) + fp4_align(2 * G * p.n_h * 8) + fp4_align((size_t)p.B * 16);
 }
 
 int run_attend_fp4(const AttendFp4Params &p, void *ws, size_t, cudaStream_t s) {
@@ -730,8 +749,8 @@ int run_attend_fp4(const AttendFp4Params &p, void *ws, size_t, cudaStream_t s) {
   pl.fd_cap = make_fastdiv((uint32_t)std::max(p.cap, 1));
   if (pl.G > 1) {
     char *w = static_cast<char *>(ws);
-    pl.part_o = reinterpret_cast<float *>(w);
-    w += fp4_align((size_t)2 * pl.G * p.n_h * p.c * 4);
+    pl.part_o = reinterpret_cast<float4 *>(w);
+    w += fp4_part_bytes(p, pl.G);
     pl.part_ml = reinterpret_cast<float2 *>(w);
     w += fp4_align((size_t)2 * pl.G * p.n_h * 8);
     pl.meta = reinterpret_cast<int4 *>(w);
@@ -740,8 +759,7 @@ int run_attend_fp4(const AttendFp4Params &p, void *ws, size_t, cudaStream_t s) {
   if (rc || pl.G == 1) return rc;
   LaunchScope ls("attend_fp4_combine", s);
   cudaLaunchConfig_t cfg{};
-  const int heads = 512 / p.c;
-  cfg.gridDim = dim3(p.B, (p.n_h + heads - 1) / heads, 1);
+  cfg.gridDim = dim3(p.B, p.c / 32, (p.n_h + 15) / 16);
   cfg.blockDim = dim3(128, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
