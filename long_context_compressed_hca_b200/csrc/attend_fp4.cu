@@ -594,32 +594,69 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
     tmem_relinquish();
   }
   pdl_trigger();
-  // ---- this CTA's run: tiles of all sequences summed up, then the sequence where the run begins
-  int *sums = reinterpret_cast<int *>(smem + L::sum_off);
-  Fp4Run run;
   {
+    // the lists and page tables, read by whoever needs them after two more
+    // dependent loads: every CTA brings a part of them into L2
+    const long long line = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (p.idx && line * 32 < (long long)p.B * p.k) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.idx + line * 32));
+    if (p.pages && line * 32 < (long long)p.B * p.max_pages) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.pages + line * 32));
+  }
+  // ---- this CTA's run: tiles of all sequences summed up, then the sequence where the run begins
+  Fp4Run run;
+  auto cut = [&](int total) {
+    run.base = total / pl.G;
+    run.rem = total - run.base * pl.G;
+    run.before = blockIdx.x * run.base + min((int)blockIdx.x, run.rem);
+    run.n = run.base + ((int)blockIdx.x < run.rem ? 1 : 0);
+    run.b0 = run.j0 = 0;
+  };
+  // inclusive sum over the warp's lanes
+  auto scan = [&](int x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  if (p.B <= 128) {
+    // every warp for itself: 4 sequences per lane
+    int nt[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = 4 * lane + i;
+      nt[i] = b < p.B ? fp4_keys(p, pl, b).nt : 0;
+      mine += nt[i];
+    }
+    const int upto = scan(mine);
+    cut(__shfl_sync(0xffffffffu, upto, 31));
+    int first = upto - mine, b0 = -1, j0 = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (nt[i] > 0 && run.before >= first && run.before < first + nt[i]) {
+        b0 = 4 * lane + i;
+        j0 = run.before - first;
+      }
+      first += nt[i];
+    }
+    const uint32_t has = __ballot_sync(0xffffffffu, b0 >= 0);
+    const int src = has ? __ffs(has) - 1 : 0;
+    run.b0 = __shfl_sync(0xffffffffu, b0, src);
+    run.j0 = __shfl_sync(0xffffffffu, j0, src);
+  } else {
     constexpr int NW = kThreads / 32;
+    int *sums = reinterpret_cast<int *>(smem + L::sum_off), *at = reinterpret_cast<int *>(smem + L::run_off);
     int mine = 0;
     for (int b = threadIdx.x; b < p.B; b += kThreads) mine += fp4_keys(p, pl, b).nt;
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (lane == 0) sums[warp] = mine;
     __syncthreads();
-    const int total = __reduce_add_sync(0xffffffffu, lane < NW ? sums[lane] : 0);
-    run.base = total / pl.G;
-    run.rem = total - run.base * pl.G;
-    run.before = blockIdx.x * run.base + min((int)blockIdx.x, run.rem);
-    run.n = run.base + ((int)blockIdx.x < run.rem ? 1 : 0);
-    int *at = reinterpret_cast<int *>(smem + L::run_off);
+    cut(__reduce_add_sync(0xffffffffu, lane < NW ? sums[lane] : 0));
     int done = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
       const int nt = b < p.B ? fp4_keys(p, pl, b).nt : 0;
-      int x = nt;                         // inclusive scan over the warp, then over the warps
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
+      const int x = scan(nt);
       __syncthreads();
       if (lane == 31) sums[warp] = x;
       __syncthreads();
@@ -631,12 +668,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
       }
       done += __reduce_add_sync(0xffffffffu, t);
     }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    run.b0 = run.n > 0 ? at[0] : 0;
-    run.j0 = run.n > 0 ? at[1] : 0;
+    if (run.n > 0) {
+      run.b0 = at[0];
+      run.j0 = at[1];
+    }
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
 
   if (warp >= kLoad0) {
@@ -711,12 +751,18 @@ __global__ void __launch_bounds__(128) fp4_combine_kernel(AttendFp4Params p, Fp4
       make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 
-// CTAs of a call: the budget, no more than there can be tiles; ne: entry slots of a sequence.
-int fp4_ctas(const AttendFp4Params &p, int ne) {
+// CTAs of a call: the budget, no more than there can be tiles.  A part costs
+// its n_h x c sums written and read again, so a CTA gets at least as many tiles
+// as keep that small beside them (64 x 512: 4), and listed entries, whose count
+// is known here, are cut into equal parts of each sequence: 32 sequences of 10
+// tiles at 64 x 512 take 27.5 us on 64 CTAs, 31 on 32 (whole sequences), 96 and
+// 148; one sequence of 10 tiles at 16 x 128 takes 11.2 us on 10 CTAs, 13.2 on 3.
+int fp4_ctas(const AttendFp4Params &p, int ne, bool listed) {
   const int sms = num_sms(), budget = p.max_ctas > 0 && p.max_ctas < sms ? p.max_ctas : sms;
-  const int nw = std::min(p.w, p.max_pos + 1);
-  const long long tiles = (long long)p.B * ((nw + KT - 1) / KT + (ne + KT - 1) / KT);
-  return (int)std::max<long long>(1, std::min<long long>(budget, tiles));
+  const int nw = std::min(p.w, p.max_pos + 1), tiles = (nw + KT - 1) / KT + (ne + KT - 1) / KT;
+  const int least = std::max(1, p.n_h * p.c / 8192);
+  if (listed && p.B <= budget) return p.B * std::max(1, std::min(budget / p.B, tiles / least));
+  return (int)std::max<long long>(1, std::min<long long>(budget, std::max<long long>(std::min(p.B, budget), (long long)p.B * tiles / least)));
 }
 size_t fp4_align(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t fp4_part_bytes(const AttendFp4Params &p, size_t G) { return fp4_align(2 * G * ((p.n_h + 15) / 16 * 16) * p.c * 4); }
@@ -738,13 +784,13 @@ int launch_fp4(const AttendFp4Params &p, const Fp4Plan &pl, cudaStream_t s) {
 
 // One CTA finishes every sequence itself and needs no workspace.
 size_t attend_fp4_workspace_bytes(const AttendFp4Params &p) {
-  const size_t G = (size_t)fp4_ctas(p, std::max(p.k, (p.max_pos + 1) / p.m));   // listed or not
+  const size_t G = (size_t)std::max(fp4_ctas(p, p.k, true), fp4_ctas(p, (p.max_pos + 1) / p.m, false));   // listed or not
   return G == 1 ? 0 : fp4_part_bytes(p, G) + fp4_align(2 * G * p.n_h * 8) + fp4_align((size_t)p.B * 16);
 }
 
 int run_attend_fp4(const AttendFp4Params &p, void *ws, size_t, cudaStream_t s) {
   Fp4Plan pl{};
-  pl.G = fp4_ctas(p, p.idx ? p.k : (p.max_pos + 1) / p.m);
+  pl.G = p.idx ? fp4_ctas(p, p.k, true) : fp4_ctas(p, (p.max_pos + 1) / p.m, false);
   pl.fd_m = make_fastdiv((uint32_t)p.m);
   pl.fd_cap = make_fastdiv((uint32_t)std::max(p.cap, 1));
   if (pl.G > 1) {
