@@ -387,27 +387,27 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
   uint32_t kph = 0;
   int before = run.before;
 
-  for (Fp4Walk w = fp4_walk(run); fp4_next(p, pl, run, w); ++npiece) {
-    // ---- Q into tensor memory (the previous piece's last S has been read)
-    if (npiece > 0 && !mbar_wait_fast(bar(bars->q_empty), (npiece - 1) & 1, p.status)) return;
+  auto write_q = [&](int b) {             // Q into tensor memory
     tc_fence_after();
-    {
-      const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((long long)w.b * p.n_h + (live ? r : 0)) * C + half * (C / 2));
-      const uint32_t tq = tmem + lane_S + L::q_col;
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((long long)b * p.n_h + (live ? r : 0)) * C + half * (C / 2));
+    const uint32_t tq = tmem + lane_S + L::q_col;
 #pragma unroll 1
-      for (int b0 = 0; b0 < C / 16; b0 += 8) {
-        uint4 v[8];
+    for (int b0 = 0; b0 < C / 16; b0 += 8) {
+      uint4 v[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) v[x] = live ? __ldg(src + b0 + x) : make_uint4(0, 0, 0, 0);
-        tmem_st_16x32bx2_x16<C / 4>(tq + 4 * b0, *reinterpret_cast<const uint32_t(*)[16]>(&v[0]));
-        tmem_st_16x32bx2_x16<C / 4>(tq + 4 * b0 + 16, *reinterpret_cast<const uint32_t(*)[16]>(&v[4]));
-      }
+      for (int x = 0; x < 8; ++x) v[x] = live ? __ldg(src + b0 + x) : make_uint4(0, 0, 0, 0);
+      tmem_st_16x32bx2_x16<C / 4>(tq + 4 * b0, *reinterpret_cast<const uint32_t(*)[16]>(&v[0]));
+      tmem_st_16x32bx2_x16<C / 4>(tq + 4 * b0 + 16, *reinterpret_cast<const uint32_t(*)[16]>(&v[4]));
     }
     tmem_st_wait();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(bars->q_full));
-
+  };
+  Fp4Walk w = fp4_walk(run);
+  bool more = fp4_next(p, pl, run, w);
+  if (more) write_q(w.b);
+  for (; more; ++npiece) {
     float m_used = -INFINITY, l = 0.f;    // running maximum (log2 units; -inf until a key is seen), sum of this half
     for (int j = 0; j < w.cnt; ++j, ++g) {
       const int st = g % SP;
@@ -484,6 +484,13 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
       if (lane == 0) mbar_arrive(bar(bars->p_full[st]));
     }
 
+    // the next piece's Q before this one's epilogue, so that its first S need not wait for that
+    Fp4Walk wn = w;
+    more = fp4_next(p, pl, run, wn);
+    if (more) {
+      if (!mbar_wait_fast(bar(bars->q_empty), npiece & 1, p.status)) return;
+      write_q(wn.b);
+    }
     // ---- epilogue
     const bool whole = w.cnt == w.k.nt;
     const float ltot = l + __shfl_xor_sync(0xffffffffu, l, 16);
@@ -562,6 +569,7 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(bars->o_empty));
     before += w.cnt;
+    w = wn;
   }
 }
 
