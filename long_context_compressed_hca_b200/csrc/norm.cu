@@ -4,11 +4,18 @@
 //   z = x + res,  y = z * gamma / sqrt(mean z^2 + eps),
 //   e4m3: scale = amax|y| / 448 over a row or a group, code = e4m3(y / scale).
 //
-// One block per row holds the row in registers (8 C channels per thread), so
-// every input is read once and every output written once.  A row-wide e4m3
-// scale needs amax|y| = max|z gamma| / sqrt(..), which is reduced together
-// with the sum of squares: one block reduction either way.  Group scales are
-// maxima over 8 or 16 neighbouring lanes.
+// A block holds a row in registers (8 C channels per thread), so every input
+// is read once and every output written once.  A row-wide e4m3 scale needs
+// amax|y| = max|z gamma| / sqrt(..), which is reduced together with the sum of
+// squares: one block reduction either way.  Group scales are maxima over 8 or
+// 16 neighbouring lanes.  Bound: HBM.  With many rows a block takes several:
+// gamma stays in registers (read again for every row it is as many bytes as x
+// and res in bf16) and the next row's loads are on their way while this one is
+// reduced and written (16411 x 4104 bf16: 98 us, 127 with a block per row).
+// Rows beyond 8192 channels take 4 times 8 channels per thread, for which the
+// registers hold neither gamma nor another row.
+#include <algorithm>
+
 #include "internal.h"
 #include "lowbit.cuh"
 
@@ -42,101 +49,154 @@ struct E4M3 {
   unsigned char b;
 };
 
-template <typename XT, typename RT, typename OT, int C>
-__global__ void __launch_bounds__(1024)
-    add_rms_norm_kernel(NormParams p) {
-  constexpr bool kFp8 = sizeof(OT) == 1;
-  __shared__ float2 part[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
-  const long long r = blockIdx.x;
-  const XT *x = static_cast<const XT *>(p.x) + r * p.ldx;
-  const RT *res = static_cast<const RT *>(p.res) + r * p.ldr;
-  RT *ro = static_cast<RT *>(p.res_out) + r * p.ldr;
+// Eight channels as they lie in memory: 16 bytes of bf16 or 32 of f32.
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T *p, int n, bool vec) {
+  Raw8<T> r;
+  if (vec && n >= 8) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    return r;
+  }
+  T t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : T(0.f);
+  memcpy(&r, t, sizeof r);
+  return r;
+}
+__device__ __forceinline__ void unpack8(const Raw8<float> &r, float (&v)[8]) { memcpy(v, &r, sizeof v); }
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
 
-  float z[C][8], g[C][8];
-  float ss = 0.f, am = 0.f;
+template <typename XT, typename RT, typename OT, int C>
+__global__ void __launch_bounds__(C <= 2 ? 512 : 1024) add_rms_norm_kernel(NormParams p) {
+  constexpr bool kFp8 = sizeof(OT) == 1, kAhead = C <= 2;
+  __shared__ float2 parts[2][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
+  // res may be res_out: a row of it is read before any thread of its block writes it, and by no other block
+  Raw8<XT> xr[C];
+  Raw8<RT> rr[C];
+  auto load = [&](long long r) {
 #pragma unroll
-  for (int j = 0; j < C; ++j) {
-    const int e = 8 * (tid + j * nthr), n = p.d - e;
-    load_row8(x + e, n, p.vec, z[j]);
-    if (p.res) {
-      float a[8];
-      load_row8(res + e, n, p.vec, a);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[j][i] += a[i];
+    for (int j = 0; j < C; ++j) {
+      const int e = 8 * (tid + j * nthr), n = p.d - e;
+      xr[j] = load_raw8(static_cast<const XT *>(p.x) + r * p.ldx + e, n, p.vec);
+      if (p.res) rr[j] = load_raw8(static_cast<const RT *>(p.res) + r * p.ldr + e, n, p.vec);
     }
-    if (p.gamma) load_row8(p.gamma + e, n, true, g[j]);
+  };
+  auto load_g = [&](int j, float (&g)[8]) {
+    const int e = 8 * (tid + j * nthr);
+    if (p.gamma) load_row8(p.gamma + e, p.d - e, true, g);
     else
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[j][i] = 1.f;
+      for (int i = 0; i < 8; ++i) g[i] = 1.f;
+  };
+  float g[kAhead ? C : 1][8];
+  if constexpr (kAhead) {
+    load(blockIdx.x);
+#pragma unroll
+    for (int j = 0; j < C; ++j) load_g(j, g[j]);
   }
+  int it = 0;
+  for (long long r = blockIdx.x; r < p.rows; r += gridDim.x, it ^= 1) {
+    float z[C][8];
+    float ss = 0.f, am = 0.f;
+    RT *ro = static_cast<RT *>(p.res_out) + r * p.ldr;
+    if constexpr (!kAhead) load(r);
 #pragma unroll
-  for (int j = 0; j < C; ++j) {
-    const int e = 8 * (tid + j * nthr), n = p.d - e;
-    if (p.res_out) store_row8(ro + e, n, p.vec, z[j]);
+    for (int j = 0; j < C; ++j) {
+      unpack8(xr[j], z[j]);
+      if (p.res) {
+        float a[8];
+        unpack8(rr[j], a);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ss += z[j][i] * z[j][i];
-      z[j][i] *= g[j][i];
-      if (kFp8) am = fmaxf(am, fabsf(z[j][i]));
+        for (int i = 0; i < 8; ++i) z[j][i] += a[i];
+      }
     }
-  }
-  ss = warp_sum(ss);
-  if (kFp8) am = warp_max(am);
-  if (lane == 0) part[warp] = make_float2(ss, am);
-  __syncthreads();
-  const float2 q = lane < (nthr >> 5) ? part[lane] : make_float2(0.f, 0.f);
-  ss = warp_sum(q.x);
-  if (kFp8) am = warp_max(q.y);
-  const float rstd = 1.0f / sqrtf(ss / (float)p.d + p.eps);
+    if constexpr (kAhead)
+      if (r + gridDim.x < p.rows) load(r + gridDim.x);
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int e = 8 * (tid + j * nthr), n = p.d - e;
+      if (p.res_out) store_row8(ro + e, n, p.vec, z[j]);
+      float(&gj)[8] = g[kAhead ? j : 0];
+      if constexpr (!kAhead) load_g(j, gj);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        ss += z[j][i] * z[j][i];
+        z[j][i] *= gj[i];
+        if (kFp8) am = fmaxf(am, fabsf(z[j][i]));
+      }
+    }
+    ss = warp_sum(ss);
+    if (kFp8) am = warp_max(am);
+    float2 *part = parts[it];
+    if (lane == 0) part[warp] = make_float2(ss, am);
+    __syncthreads();
+    const float2 q = lane < (nthr >> 5) ? part[lane] : make_float2(0.f, 0.f);
+    ss = warp_sum(q.x);
+    if (kFp8) am = warp_max(q.y);
+    const float rstd = 1.0f / sqrtf(ss / (float)p.d + p.eps);
 
-  float scale = 0.f;
-  if (kFp8 && p.group == 0) {
-    scale = __fdiv_rn(am * rstd, 448.0f);
-    if (tid == 0) p.out_scale[r] = scale;
-  }
+    float scale = 0.f;
+    if (kFp8 && p.group == 0) {
+      scale = __fdiv_rn(am * rstd, 448.0f);
+      if (tid == 0) p.out_scale[r] = scale;
+    }
 #pragma unroll
-  for (int j = 0; j < C; ++j) {
-    const int e = 8 * (tid + j * nthr), n = p.d - e;
+    for (int j = 0; j < C; ++j) {
+      const int e = 8 * (tid + j * nthr), n = p.d - e;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[j][i] *= rstd;
-    if constexpr (kFp8) {
-      if (p.group) {
-        float m = 0.f;
+      for (int i = 0; i < 8; ++i) z[j][i] *= rstd;
+      if constexpr (kFp8) {
+        if (p.group) {
+          float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(z[j][i]));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-        if (p.group == 128) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        scale = __fdiv_rn(m, 448.0f);
-        if (n > 0 && e % p.group == 0) p.out_scale[r * (p.d / p.group) + e / p.group] = scale;
+          for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(z[j][i]));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          if (p.group == 128) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          scale = __fdiv_rn(m, 448.0f);
+          if (n > 0 && e % p.group == 0) p.out_scale[r * (p.d / p.group) + e / p.group] = scale;
+        }
+        if (n <= 0) continue;
+        uint32_t w[2] = {0u, 0u};
+        if (scale > 0.f) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i >> 2] |= f32_e4m3(__fdiv_rn(z[j][i], scale)) << (8 * (i & 3));
+        }
+        unsigned char *o = static_cast<unsigned char *>(p.out) + r * p.ldo + e;
+        if (p.vec && n >= 8) *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+        else
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < n) o[i] = (unsigned char)(w[i >> 2] >> (8 * (i & 3)));
+      } else {
+        if (n > 0) store_row8(static_cast<OT *>(p.out) + r * p.ldo + e, n, p.vec, z[j]);
       }
-      if (n <= 0) continue;
-      uint32_t w[2] = {0u, 0u};
-      if (scale > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i >> 2] |= f32_e4m3(__fdiv_rn(z[j][i], scale)) << (8 * (i & 3));
-      }
-      unsigned char *o = static_cast<unsigned char *>(p.out) + r * p.ldo + e;
-      if (p.vec && n >= 8) *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
-      else
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < n) o[i] = (unsigned char)(w[i >> 2] >> (8 * (i & 3)));
-    } else {
-      if (n > 0) store_row8(static_cast<OT *>(p.out) + r * p.ldo + e, n, p.vec, z[j]);
     }
   }
 }
 
 template <typename XT, typename RT, typename OT>
 int launch_norm_t(const NormParams &p, cudaStream_t s) {
-  // threads of 8 channels up to 512 of them, then more channels per thread
+  // threads of 8 channels up to 512 of them, then of 16, then (up to 1024 threads) of 32
   const int units = (p.d + 7) / 8;
   const int C = units <= 512 ? 1 : units <= 1024 ? 2 : 4;
   const int thr = ((units + C - 1) / C + 31) / 32 * 32;
-  const unsigned grid = (unsigned)p.rows;
+  // as many blocks as the SMs can hold threads of
+  const unsigned grid = (unsigned)std::min<long long>(p.rows, (long long)num_sms() * (2048 / thr));
   if (C == 1) return HCA_LAUNCH("add_rms_norm", s, add_rms_norm_kernel<XT, RT, OT, 1><<<grid, thr, 0, s>>>(p));
   if (C == 2) return HCA_LAUNCH("add_rms_norm", s, add_rms_norm_kernel<XT, RT, OT, 2><<<grid, thr, 0, s>>>(p));
   return HCA_LAUNCH("add_rms_norm", s, add_rms_norm_kernel<XT, RT, OT, 4><<<grid, thr, 0, s>>>(p));
