@@ -87,8 +87,11 @@ __global__ void __launch_bounds__(kFp4KvWarps * 32)
         const int e = fp4_block_exp(amax);
         eb = (uint32_t)(e + 127);
         const float inv = pow2f(-e);     // -126 <= -e <= 126: exact products
+        float q[2][8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i >> 3] |= e2m1_code(v[i] * inv) << (4 * (i & 7));
+        for (int i = 0; i < 16; ++i) q[i >> 3][i & 7] = v[i] * inv;
+        w[0] = e2m1x8_code(q[0]);
+        w[1] = e2m1x8_code(q[1]);
       }
       *reinterpret_cast<uint2 *>(rp + 8 * lr.u) = make_uint2(w[0], w[1]);
       if ((lr.u & 1) == 0) rp[soff + (lr.u >> 1)] = (unsigned char)eb;

@@ -83,6 +83,21 @@ __device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, in
   }
 }
 
+// The codes of eight values, v[i] in nibble i: the conversion instruction's
+// nearest, ties to even, saturating; zero as +0.
+__device__ __forceinline__ uint32_t e2m1x8_code(const float (&v)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 x<4>;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 x0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 x1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 x2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 x3, %8, %7;\n\t"
+      "mov.b32 %0, {x0, x1, x2, x3};\n\t}"
+      : "=r"(w) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  const uint32_t some = (w | (w >> 1) | (w >> 2)) & 0x11111111u;   // a magnitude bit
+  return w & (0x77777777u | (some << 3));
+}
+
 // One lane of a converged warp.  A role that runs warp-uniform up to this
 // choice keeps MMA descriptors in uniform registers; one that runs on a lane
 // of its own moves each of them there again for every instruction.
