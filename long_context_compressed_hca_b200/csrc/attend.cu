@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(128) attend_combine(AttendParams p) {
 #pragma unroll 4
     for (int sp = 0; sp < p.nsplit; ++sp) {
       const float w = wsc[hh][sp];
+      if (w == 0.f) continue;   // an empty split's part was never written
       const float4 v = *reinterpret_cast<const float4 *>(base + (long long)sp * 64 * C);
       acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
     }
