@@ -6,6 +6,7 @@ device memory and streams.  Loading fails loudly if libhca.so is missing.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import re
 
@@ -558,13 +559,14 @@ def w4_quantize(d: W4Desc, w, stream=None):
     return codes, scales, row_scale
 
 
+@functools.lru_cache(maxsize=None)
 def kv_fp4_row_bytes(c, rd) -> int:
     """Bytes of one row's 4-bit record (0 = unsupported)."""
     return lib().hca_kv_fp4_row_bytes(c, rd)
 
 
 def _fp4_records(name, t, c, rd, dev):
-    rec = lib().hca_kv_fp4_row_bytes(c, rd)
+    rec = kv_fp4_row_bytes(c, rd)
     if rec == 0:
         _bad(f"unsupported (c, rd) = ({c}, {rd})")
     return _tensor(name, t, t.shape[:-1] + (rec,), _U8, dev), t.numel() // rec

@@ -79,39 +79,46 @@ __device__ __forceinline__ void w4_decode(const uint4 &q, uint32_t s2, uint32_t 
 // ---------------------------------------------------------------- x in f16
 // Row (g, t) of the workspace: K f16 values, zeros up to Kp, and the factor
 // that the sum over them is multiplied by.
+// One block per row, up to 1024 threads, each with up to 4 times 8 values, so
+// that a row is read once.
+constexpr int kXChunks = 4;
 template <int CODE, typename XT>
-__global__ void __launch_bounds__(256) w4_x_kernel(W4Params p, __half *xh, float *xd, int Kp) {
-  __shared__ float part[8];
+__global__ void __launch_bounds__(1024) w4_x_kernel(W4Params p, __half *xh, float *xd, int Kp) {
+  __shared__ float part[32];
   pdl_trigger();   // the product kernel may start on its weights
-  const int r = blockIdx.x, g = r / p.T, t = r - g * p.T, tid = threadIdx.x;
+  const int r = blockIdx.x, g = r / p.T, t = r - g * p.T, tid = threadIdx.x, nthr = blockDim.x;
   const XT *x = static_cast<const XT *>(p.x) + (long long)t * p.ldx + (long long)g * p.K;
   uint4 *o = reinterpret_cast<uint4 *>(xh + (long long)r * Kp);
   if constexpr (sizeof(XT) == 1) {
-    for (int k = tid; k < Kp / 8; k += 256)
-      o[k] = w4_x8<CODE>(8 * k < p.K ? reinterpret_cast<const uint2 *>(x)[k] : make_uint2(0, 0));
+    for (int k = tid; k < Kp / 8; k += nthr)
+      o[k] = w4_x8<CODE>(8 * k < p.K ? __ldg(reinterpret_cast<const uint2 *>(x) + k) : make_uint2(0, 0));
     if (tid == 0) xd[r] = p.x_scale[t];
   } else {
-    float am = 0.f;
-    for (int k = 8 * tid; k < p.K; k += 8 * 256) {
-      float v[8];
-      load8(x + k, v);
+    uint4 u[kXChunks];
+    uint32_t am = 0u;    // |x| as bits, in the order of the values
 #pragma unroll
-      for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(v[i]));
+    for (int i = 0; i < kXChunks; ++i) {
+      const int k = tid + i * nthr;
+      u[i] = 8 * k < p.K ? __ldg(reinterpret_cast<const uint4 *>(x) + k) : make_uint4(0, 0, 0, 0);
     }
-    am = warp_max(am);
-    if ((tid & 31) == 0) part[tid >> 5] = am;
+#pragma unroll
+    for (int i = 0; i < kXChunks; ++i)
+      am = __vmaxu2(am, __vmaxu2(__vmaxu2(u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu),
+                                 __vmaxu2(u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu)));
+    am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
+    uint32_t *top = reinterpret_cast<uint32_t *>(part);
+    if ((tid & 31) == 0) top[tid >> 5] = am;
     __syncthreads();
-    am = part[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) am = fmaxf(am, part[i]);
-    // e: am = f * 2^e, 1 <= f < 2, not below -110 so that 2^(14 - e) and its inverse are normal
-    const int e = max((int)((__float_as_uint(am) >> 23) & 0xFFu) - 127, -110);
+    am = __reduce_max_sync(0xffffffffu, (tid & 31) < (nthr >> 5) ? top[tid & 31] : 0u);
+    // 2^e <= the largest value < 2^(e + 1), e at least -110 so that 2^(14 - e) and its inverse are normal
+    const int e = max((int)(am >> 7) - 127, -110);
     const float up = pow2f(14 - e);
-    for (int k = tid; k < Kp / 8; k += 256) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (8 * k < p.K) load8(x + 8 * k, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= up;
+    for (int i = 0; i < kXChunks; ++i) {
+      const int k = tid + i * nthr;
+      if (8 * k >= Kp) break;
+      const float v[8] = {bf16_lo(u[i].x) * up, bf16_hi(u[i].x) * up, bf16_lo(u[i].y) * up, bf16_hi(u[i].y) * up,
+                          bf16_lo(u[i].z) * up, bf16_hi(u[i].z) * up, bf16_lo(u[i].w) * up, bf16_hi(u[i].w) * up};
       o[k] = w4_x8<CODE>(v);
     }
     if (tid == 0) xd[r] = pow2f(e - 14);
@@ -645,7 +652,8 @@ int launch_w4_t(const W4Params &p, cudaStream_t s) {
                         (uint64_t)l.Kp * 2, 64, TN, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc) return rc;
   if (wk.x == kRing) {
-    rc = HCA_LAUNCH("w4_x", s, w4_x_kernel<CODE, XT><<<(unsigned)p.groups * p.T, 256, 0, s>>>(p, xh, xd, l.Kp));
+    const int thr = std::min(1024, l.Kp / 8);   // Kp is a multiple of 256, at most 32768
+    rc = HCA_LAUNCH("w4_x", s, w4_x_kernel<CODE, XT><<<(unsigned)p.groups * p.T, thr, 0, s>>>(p, xh, xd, l.Kp));
     if (rc) return rc;
   } else {
     tmX = tmC;      // not used
