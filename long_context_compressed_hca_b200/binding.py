@@ -6,7 +6,6 @@ device memory and streams.  Loading fails loudly if libhca.so is missing.
 from __future__ import annotations
 
 import ctypes as C
-import functools
 import os
 import re
 
@@ -458,43 +457,27 @@ def output_projection(d: OprojDesc, o, wo_a, wo_b, out, ws, stream=None):
 
 # ------------------------------------------------------- the low-bit decode step
 # These calls take tensors only and check them (device, type, shape, layout)
-# before the library sees their addresses.
+# before the library sees their addresses; csrc/host/torch_call.cpp does it.
+_call_module = None
+
+
+def _call():
+    """The extension module with the checked calls (raises if it has not been built)."""
+    global _call_module
+    if _call_module is None:
+        lib()
+        try:
+            from . import _torch_call as m
+        except ImportError as e:
+            raise HcaError(HCA_ERR_UNSUPPORTED, f"_torch_call.so cannot be loaded ({e}): build it with "
+                           "`python -m long_context_compressed_hca_b200.build`") from e
+        m.set_error(HcaError)
+        _call_module = m
+    return _call_module
+
+
 def _bad(msg):
     raise HcaError(HCA_ERR_INVALID, msg)
-
-
-_CODE_TYPES = {HCA_F32: (torch.float32,), HCA_BF16: (torch.bfloat16,),
-               HCA_FP8E4M3: (torch.float8_e4m3fn, torch.uint8)}
-_F32, _BF16, _U8, _I32, _I64 = ((t,) for t in (torch.float32, torch.bfloat16, torch.uint8, torch.int32, torch.int64))
-
-
-def _tensor(name, t, shape, types, dev, ld=0):
-    """Address of t, which is on device dev, of one of the types and the shape; dense, or with rows ld elements apart."""
-    if t.get_device() == dev and t.dtype in types and t.shape == shape and (
-            t.is_contiguous() if not ld else
-            (shape[1] == 1 or t.stride(1) == 1) and (shape[0] <= 1 or t.stride(0) == ld)):
-        return t.data_ptr()
-    if t.get_device() != dev:
-        _bad(f"{name} must be on the current CUDA device (it is on {t.device})")
-    if t.dtype not in types:
-        _bad(f"{name} has dtype {t.dtype}, expected {types[0] if types else 'another'}")
-    if t.shape != shape:
-        _bad(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    _bad(f"{name} must have contiguous rows {ld} elements apart" if ld else f"{name} must be contiguous")
-
-
-def _device(t):
-    """The current device, which has to be the one of t."""
-    if not t.is_cuda:
-        _bad("tensors must be on the current CUDA device (one is on the host)")
-    return torch.cuda.current_device()
-
-
-def _scratch(ws, dev):
-    """(address, bytes) of a workspace tensor, or of none."""
-    if ws is None:
-        return None, 0
-    return _tensor("ws", ws, ws.shape, (ws.dtype,), dev), ws.numel() * ws.element_size()
 
 
 def norm_desc(rows, d, x_dtype=HCA_BF16, res_dtype=None, out_dtype=HCA_BF16, scale_group=0, eps=1e-6, ldx=0, ldr=0,
@@ -505,20 +488,7 @@ def norm_desc(rows, d, x_dtype=HCA_BF16, res_dtype=None, out_dtype=HCA_BF16, sca
 
 def add_rms_norm(d: NormDesc, x, res, gamma, res_out, out, out_scale=None, stream=None):
     """out = RMSNorm(x + res) * gamma (e4m3 with out_scale, or bf16 / f32), res_out = x + res; see hca_add_rms_norm."""
-    dev, width, od = _device(x), d.d, d.out_dtype
-    shape, rt, ldr = (d.rows, width), _CODE_TYPES.get(d.res_dtype, ()), d.ldr
-    px = _tensor("x", x, shape, _CODE_TYPES.get(d.x_dtype, ()), dev, d.ldx)
-    pr = None if res is None else _tensor("res", res, shape, rt, dev, ldr)
-    pro = None if res_out is None else _tensor("res_out", res_out, shape, rt, dev, ldr)
-    pg = None if gamma is None else _tensor("gamma", gamma, (width,), _F32, dev)
-    po = _tensor("out", out, shape, _CODE_TYPES.get(od, ()), dev, d.ldo)
-    ps = None
-    if od == HCA_FP8E4M3:
-        if out_scale is None:
-            _bad("an e4m3 output needs out_scale")
-        group = d.scale_group
-        ps = _tensor("out_scale", out_scale, (shape[0], width // group if group > 0 else 1), _F32, dev)
-    return check(lib().hca_add_rms_norm(d, px, pr, pg, pro, po, ps, stream_handle(stream)))
+    return _call().add_rms_norm(d, x, res, gamma, res_out, out, out_scale, stream)
 
 
 def w4_desc(T, N, K, groups=1, scale_group=32, code=HCA_W4_E2M1, x_dtype=HCA_BF16, out_dtype=HCA_BF16, ldx=0,
@@ -531,63 +501,39 @@ def w4_linear_workspace_size(d: W4Desc) -> int:
 
 
 def w4_linear(d: W4Desc, x, x_scale, codes, scales, row_scale, out, ws, stream=None):
-    """out = x @ W^T for 4-bit weights (w4_quantize) and T tokens; see hca_w4_linear."""
-    dev, T, N, K, groups = _device(x), d.T, d.N, d.K, d.groups
-    px = _tensor("x", x, (T, groups * K), _CODE_TYPES.get(d.x_dtype, ()), dev, d.ldx)
-    ps = None
-    if x_scale is not None:
-        if x_scale.dim() == 2:          # one scale per row as add_rms_norm writes them
-            x_scale = x_scale.view(-1)
-        ps = _tensor("x_scale", x_scale, (T,), _F32, dev)
-    pc = _tensor("codes", codes, (groups * N, K // 2), _U8, dev)
-    pw = _tensor("scales", scales, (groups, K // max(d.scale_group, 1), (N + 15) // 16 * 16), _CODE_TYPES[HCA_FP8E4M3], dev)
-    pr = _tensor("row_scale", row_scale, (groups * N,), _F32, dev)
-    po = _tensor("out", out, (T, groups * N), _CODE_TYPES.get(d.out_dtype, ()), dev, d.ldo)
-    pws, nws = _scratch(ws, dev)
-    return check(lib().hca_w4_linear(d, px, ps, pc, pw, pr, po, pws, nws, stream_handle(stream)))
+    """out = x @ W^T for 4-bit weights (w4_quantize) and T tokens; see hca_w4_linear.  x_scale [T], or [T, 1] as
+    add_rms_norm writes it."""
+    return _call().w4_linear(d, x, x_scale, codes, scales, row_scale, out, ws, stream)
 
 
 def w4_quantize(d: W4Desc, w, stream=None):
     """(codes, scales, row_scale) of weights w [groups*N, K], as w4_linear takes them."""
-    pw = _tensor("w", w, (d.groups * d.N, d.K), (torch.float32, torch.bfloat16), _device(w))
+    if not w.is_cuda or w.get_device() != torch.cuda.current_device():
+        _bad(f"w must be on the current CUDA device (it is on {w.device})")
+    if w.dtype not in (torch.float32, torch.bfloat16) or w.shape != (d.groups * d.N, d.K) or not w.is_contiguous():
+        _bad(f"w must be contiguous float32 or bfloat16 of shape {(d.groups * d.N, d.K)}, got {w.dtype} {tuple(w.shape)}")
     codes = torch.empty(d.groups * d.N, d.K // 2, dtype=torch.uint8, device=w.device)
     scales = torch.empty(d.groups, d.K // max(d.scale_group, 1), (d.N + 15) // 16 * 16, dtype=torch.uint8,
                          device=w.device)
     row_scale = torch.empty(d.groups * d.N, dtype=torch.float32, device=w.device)
-    check(lib().hca_w4_quantize(d, pw, DTYPE_CODE[w.dtype], ptr(codes), ptr(scales), ptr(row_scale),
+    check(lib().hca_w4_quantize(d, ptr(w), DTYPE_CODE[w.dtype], ptr(codes), ptr(scales), ptr(row_scale),
                                 stream_handle(stream)))
     return codes, scales, row_scale
 
 
-@functools.lru_cache(maxsize=None)
 def kv_fp4_row_bytes(c, rd) -> int:
     """Bytes of one row's 4-bit record (0 = unsupported)."""
     return lib().hca_kv_fp4_row_bytes(c, rd)
 
 
-def _fp4_records(name, t, c, rd, dev):
-    rec = kv_fp4_row_bytes(c, rd)
-    if rec == 0:
-        _bad(f"unsupported (c, rd) = ({c}, {rd})")
-    return _tensor(name, t, t.shape[:-1] + (rec,), _U8, dev), t.numel() // rec
-
-
 def kv_quant_fp4(x, c, rd, records, slots=None, stream=None):
     """Rows x [rows, c] to 4-bit records: row r to record slots[r] (int64; r without slots)."""
-    dev, rows = _device(x), x.shape[0]
-    po, n = _fp4_records("records", records, c, rd, dev)
-    px = _tensor("x", x, (rows, c), (torch.bfloat16, torch.float32), dev)
-    ps = None if slots is None else _tensor("slots", slots, (rows,), _I64, dev)
-    return check(lib().hca_kv_quant_fp4(px, DTYPE_CODE[x.dtype], rows, c, rd, po, n, ps, stream_handle(stream)))
+    return _call().kv_quant_fp4(x, c, rd, records, slots, stream)
 
 
 def kv_dequant_fp4(records, c, rd, out, slots=None, stream=None):
     """4-bit records slots[r] (record r without slots) as bf16 rows out [rows, c]."""
-    dev, rows = _device(out), out.shape[0]
-    pi, n = _fp4_records("records", records, c, rd, dev)
-    po = _tensor("out", out, (rows, c), _BF16, dev)
-    ps = None if slots is None else _tensor("slots", slots, (rows,), _I64, dev)
-    return check(lib().hca_kv_dequant_fp4(pi, n, ps, rows, c, rd, po, stream_handle(stream)))
+    return _call().kv_dequant_fp4(records, c, rd, out, slots, stream)
 
 
 class Fp4CacheHandle:
@@ -613,19 +559,5 @@ def attend_fp4_workspace_size(d: AttnDesc, max_pos) -> int:
 
 def attend_fp4(d: AttnDesc, q, cache: Fp4CacheHandle, idx, kv_win, sink, positions, max_pos, o, ws, stream=None):
     """Decode attention over a cache of 4-bit records, one position per sequence; see hca_attend_fp4."""
-    dev, B, c = _device(q), d.B, d.c
-    shape = (B, d.n_h, c)
-    pq = _tensor("q", q, shape, _BF16, dev)
-    po = _tensor("o", o, shape, _BF16, dev)
-    _fp4_records("cache rows", cache.rows, c, d.rd, dev)
-    if cache.pages is not None:
-        _tensor("pages", cache.pages, (B, cache.pages.shape[1]), _I32, dev)
-    elif cache.rows.shape[0] != B:
-        _bad(f"the cache has {cache.rows.shape[0]} sequences, expected {B}")
-    pi = None if idx is None else _tensor("idx", idx, (B, d.k), _I32, dev)
-    pk = None if kv_win is None else _tensor("kv_win", kv_win, (B, max(d.w, 1), c), _BF16, dev)
-    ps = None if sink is None else _tensor("sink", sink, (d.n_h,), _F32, dev)
-    pp = _tensor("positions", positions, (B,), _I32, dev)
-    pws, nws = _scratch(ws, dev)
-    return check(lib().hca_attend_fp4(d, pq, cache.struct, pi, pk, ps, pp, max_pos, po, pws, nws,
-                                      stream_handle(stream)))
+    return _call().attend_fp4(d, q, cache.struct, cache.rows, cache.pages, idx, kv_win, sink, positions, max_pos, o, ws,
+                              stream)
