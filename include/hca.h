@@ -533,7 +533,9 @@ int hca_w4_quantize(const hca_w4_desc *d, const void *w, hca_dtype w_dtype, void
  * e is the smallest exponent with amax <= 6 * 2^e, at least -126 (byte 0 for
  * an all-zero block); code = nearest E2M1 (ties to the even code) of x / 2^e;
  * zero is stored as +0.  A code channel's value is code * 2^e, exactly a bf16
- * value.  Shapes as for the mixed-precision records.  Inputs must be finite.
+ * value.  Shapes as for the mixed-precision records.  Inputs must be finite
+ * (above 1.75 * 2^127 the nearest code stands for 2^128, which reads back as
+ * infinity).
  * Rows and records: row r is record slots[r] of `records` (slots NULL: record
  * r).  quant skips a row whose slot lies outside [0, records), so a slot of -1
  * drops the row; the other slots of one call must be distinct (of two rows with
@@ -567,7 +569,8 @@ typedef struct {
  * visible, lie beyond the cache's capacity or in an absent page, and idx < 0
  * are skipped; an entry listed twice in idx counts twice.
  * q, o [B, n_h, c] HCA_BF16, n_h <= 64, c in {128, 256, 512}, (c, rd) as in
- * hca_kv_fp4_row_bytes; sink [n_h] fp32, NULL = no sink; kv_mixed must be 0;
+ * hca_kv_fp4_row_bytes; sink [n_h] fp32, NULL = no sink (+infinity: zeros,
+ * -infinity: no sink for that head); kv_mixed must be 0;
  * max_ctas as in hca_attend; B times the most keys of a sequence below 2^37.
  * q and KV values must be finite.  o may not overlap an input or ws.
  * ws: scratch of hca_attend_fp4_workspace_size bytes (16-byte aligned), which

@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(128) fp4_combine_kernel(AttendFp4Params p, Fp4
     }
     const float m = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
     if (m == -INFINITY) continue;
-    const float f = exp2f(M - m);
+    const float f = M == m ? 1.f : exp2f(M - m);   // an infinite sink takes all the weight
     M = m;
     den *= f;
     acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
