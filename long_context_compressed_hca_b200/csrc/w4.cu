@@ -237,8 +237,10 @@ __device__ __forceinline__ void w4_dec_sync() { asm volatile("bar.sync 1, %0;" :
 // The weight warps' staging of x: `units` units of TN tokens as f16 in the
 // layout that the MMAs read, and the factor per token.  A warp takes a token
 // of a unit at a time, a lane 8 channels.  bf16 values whose token has its
-// largest in [1, 2^15) (among the units staged here) are stored as they are;
-// a token outside that range is stored again, scaled.
+// largest in [1, 2^15) (among the units staged here) are stored as they are:
+// f16 keeps them exactly down to 2^-17 and to 2^-25 below, half of the last
+// bit that the fp32 sum has of a term with the largest value.  A token outside
+// that range is stored again, scaled.
 template <int TN, int CODE, typename XT>
 __device__ __forceinline__ void w4_stage_x(const W4Params &p, const W4Work &wk, int u0, int units, uint8_t *xs, float *xd,
                                            uint32_t *amax) {
