@@ -2,11 +2,33 @@
 // powers of two.
 #pragma once
 
+#include <algorithm>
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "internal.h"
 
 namespace hca {
+
+// Blocks of `threads` threads that all SMs hold at once by their registers
+// (kernels without much shared memory): the grid of a kernel whose blocks
+// stride over its work, so that no partly filled wave follows the first.
+template <auto Kernel>
+int resident_blocks(int threads) {
+  static std::atomic<int> regs_dev[kMaxDevices];
+  std::atomic<int> &regs = regs_dev[device_slot()];
+  if (!regs) {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, Kernel) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return num_sms();          // the launch reports what is wrong
+    }
+    regs = (std::max(a.numRegs, 1) + 7) / 8 * 8;
+  }
+  return num_sms() * std::max(1, std::min(2048, 65536 / regs) / threads);
+}
 
 // Two f16 values (low half: low nibble) of one byte of E2M1 codes, by the
 // conversion instruction: exact.  Byte B of w.
