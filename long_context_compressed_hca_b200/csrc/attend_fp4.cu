@@ -48,13 +48,14 @@ constexpr int SP = 2;                        // S and P buffers
 // Launch-time sizes beside the call's parameters.
 struct Fp4Plan {
   int G;                   // CTAs
+  int S;                   // CTAs of a cluster that has one sequence; 0: runs over all sequences
   FastDiv fd_m, fd_cap;
   float4 *part_o;          // [2 G] parts of fp4_part's layout
   float2 *part_ml;         // [2 G][n_h]
   int4 *meta;              // [B]: first and last CTA of a cut sequence and the first one's slot; x < 0: finished
 };
 
-// A part's O: for every 16 heads and 4 columns i, i + 1, .. of either half of
+// A part's O, in the workspace or in shared memory: for every 16 heads and 4 columns i, i + 1, .. of either half of
 // the channels, the 32 threads (half, head) side by side.  float4 index of
 // heads 16 q .. and columns 4 i of part `slot`, thread 0.
 __device__ __forceinline__ long long fp4_part(const AttendFp4Params &p, long long slot, int q, int i) {
@@ -492,7 +493,7 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
       write_q(wn.b);
     }
     // ---- epilogue
-    const bool whole = w.cnt == w.k.nt;
+    const bool whole = w.cnt == w.k.nt && !pl.S;
     const float ltot = l + __shfl_xor_sync(0xffffffffu, l, 16);
     if (pl.meta && threadIdx.x == 0 && w.j == 0) {
       // the CTA that has a sequence's first tile says who else has some
@@ -518,10 +519,12 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
     float inv = 0.f;
     if (m_used != -INFINITY) inv = 1.f / (ltot + (p.sink && live ? exp2f(p.sink[r] * kLog2e - m_used) : 0.f));
     if (!whole) {
-      // 16 rows of a warp side by side, so that a store is 512 contiguous bytes
-      if (live && half == 0) pl.part_ml[slot * p.n_h + r] = make_float2(m_used, ltot);
+      // 16 rows of a warp side by side, so that a store is 512 contiguous bytes; in a cluster they go where the
+      // key tiles were
+      float2 *ml = pl.S ? reinterpret_cast<float2 *>(smem + L::p_off) : pl.part_ml + slot * p.n_h;
+      if (live && half == 0) ml[r] = make_float2(m_used, ltot);
       if (warp * 16 < p.n_h) {
-        float4 *dst = pl.part_o + fp4_part(p, slot, warp, 0) + lane;
+        float4 *dst = (pl.S ? reinterpret_cast<float4 *>(smem) + fp4_part(p, 0, warp, 0) : pl.part_o + fp4_part(p, slot, warp, 0)) + lane;
 #pragma unroll 1
         for (int c0 = 0; c0 < C / 2; c0 += 32, dst += 256) {
           uint32_t ov[32];
@@ -570,6 +573,71 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
     if (lane == 0) mbar_arrive(bar(bars->o_empty));
     before += w.cnt;
     w = wn;
+  }
+}
+
+// Joins the parts of one sequence, o = sum_i 2^(m_i - M) O_i / (sum_i 2^(m_i -
+// M) l_i + 2^(sink - M)) in their order, for head h and 4 columns from col:
+// get_ml(i) and get_o(i) are part i's statistics and sums, parts i0 .. i1.
+template <typename FM, typename FO>
+__device__ __forceinline__ float4 fp4_join(const AttendFp4Params &p, int h, int i0, int i1, FM get_ml, FO get_o) {
+  const float sink = p.sink ? p.sink[h] * kLog2e : -INFINITY;
+  // one pass with a running maximum, 4 parts at a time
+  float M = sink, den = sink == -INFINITY ? 0.f : 1.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = i0; c0 <= i1; c0 += 4) {
+    float2 ml[4];
+    float4 o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (c0 + k <= i1) {
+        ml[k] = get_ml(c0 + k);
+        o[k] = get_o(c0 + k);
+      }
+    }
+    const float m = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
+    if (m == -INFINITY) continue;
+    const float f = M == m ? 1.f : exp2f(M - m);   // an infinite sink takes all the weight
+    M = m;
+    den *= f;
+    acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (ml[k].x == -INFINITY) continue;     // a part without keys
+      const float e = exp2f(ml[k].x - M);
+      den += e * ml[k].y;
+      acc.x += e * o[k].x; acc.y += e * o[k].y; acc.z += e * o[k].z; acc.w += e * o[k].w;
+    }
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+}
+// The rotation of two pairs and the store.
+__device__ __forceinline__ void fp4_rotate_store(const AttendFp4Params &p, int b, int h, int col, float4 v, float2 cs0, float2 cs1) {
+  if (col >= p.c - p.rd)
+    v = make_float4(v.x * cs0.x + v.y * cs0.y, v.y * cs0.x - v.x * cs0.y, v.z * cs1.x + v.w * cs1.y, v.w * cs1.x - v.z * cs1.y);
+  *reinterpret_cast<uint2 *>(p.o + ((long long)b * p.n_h + h) * p.c + col) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+// A cluster's sequence: its CTAs have their parts in shared memory, and each
+// joins a share of the columns.
+template <int C>
+__device__ __forceinline__ void fp4_cluster_join(const AttendFp4Params &p, const Fp4Plan &pl, int b, uint8_t *smem) {
+  using L = Fp4Layout<C>;
+  const int lane = threadIdx.x & 31, per = C / 8 / pl.S, rank = blockIdx.x % pl.S;
+  const float2 *rope = reinterpret_cast<const float2 *>(smem + L::p_off + 1024);
+  const uint32_t sbase = smem_u32(smem);
+  for (int pair = threadIdx.x >> 5; pair < (p.n_h + 15) / 16 * per; pair += kThreads / 32) {
+    const int q = pair / per, i = rank * per + pair % per, h = 16 * q + (lane & 15), col = (lane >> 4) * (C / 2) + 4 * i;
+    if (h >= p.n_h) continue;
+    const uint32_t off = (uint32_t)(fp4_part(p, 0, q, i) + lane) * 16u;
+    const float4 v = fp4_join(
+        p, h, 0, pl.S - 1, [&](int s) { return ld_dsmem_f32x2(cluster_map(sbase + L::p_off + 8 * h, s)); },
+        [&](int s) { return ld_dsmem_f32x4(cluster_map(sbase + off, s)); });
+    const int k = (col - (C - p.rd)) / 2;
+    const bool rot = col >= C - p.rd;
+    fp4_rotate_store(p, b, h, col, v, rot ? rope[k] : make_float2(1.f, 0.f), rot ? rope[k + 1] : make_float2(1.f, 0.f));
   }
 }
 
@@ -627,7 +695,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
     }
     return x;
   };
-  if (p.B <= 128) {
+  if (pl.S) {
+    // the sequence's tiles in equal shares
+    const int nt = fp4_keys(p, pl, blockIdx.x / pl.S).nt, r = blockIdx.x % pl.S;
+    run.base = nt / pl.S;
+    run.rem = nt - run.base * pl.S;
+    run.before = 0;
+    run.n = run.base + (r < run.rem ? 1 : 0);
+    run.b0 = blockIdx.x / pl.S;
+    run.j0 = r * run.base + min(r, run.rem);
+  } else if (p.B <= 128) {
     // every warp for itself: 4 sequences per lane
     int nt[4], mine = 0;
 #pragma unroll
@@ -693,8 +770,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
     fp4_mma<C>(p, pl, run, smem_u32(smem), bars, tmem);
   } else {
     fp4_softmax<C>(p, pl, run, smem, bars, tmem);
+    if (pl.S) {
+      if (run.n == 0 && threadIdx.x < 64)   // a part without keys
+        reinterpret_cast<float2 *>(smem + L::p_off)[threadIdx.x] = make_float2(-INFINITY, 0.f);
+      for (int i = threadIdx.x; i < p.rd / 2; i += 128) {
+        float sn, cs;
+        fp4_rope(p, min(__ldg(p.positions + run.b0), p.max_pos), i, sn, cs);
+        reinterpret_cast<float2 *>(smem + L::p_off + 1024)[i] = make_float2(cs, sn);
+      }
+    }
     // sequences without keys: zeros
-    for (int b = blockIdx.x; b < p.B; b += pl.G) {
+    for (int b = pl.S ? p.B : (int)blockIdx.x; b < p.B; b += pl.G) {
       if (fp4_keys(p, pl, b).nt) continue;
       for (int i = threadIdx.x; i < p.n_h * C / 8; i += 128)
         reinterpret_cast<uint4 *>(p.o + (long long)b * p.n_h * C)[i] = make_uint4(0, 0, 0, 0);
@@ -705,58 +791,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (pl.S) {
+    // every thread of the cluster comes here, whatever its waits did
+    __syncwarp();
+    cluster_sync();
+    fp4_cluster_join<C>(p, pl, run.b0, smem);
+    __syncwarp();
+    cluster_sync();          // the parts have been read
+  }
 }
 
-// Cut sequences: o = sum_i 2^(m_i - M) O_i / (sum_i 2^(m_i - M) l_i +
-// 2^(sink - M)) over the parts in their order, rotated.  A block has 16 heads
-// and 16 columns of either half, a thread 4 of them.
+// Cut sequences' parts from the workspace.  A block has 16 heads and 16
+// columns of either half, a thread 4 of them.
 __global__ void __launch_bounds__(128) fp4_combine_kernel(AttendFp4Params p, Fp4Plan pl) {
   const int lane = threadIdx.x & 31, i = blockIdx.y * 4 + (threadIdx.x >> 5), q = blockIdx.z, b = blockIdx.x;
   const int h = 16 * q + (lane & 15), col = (lane >> 4) * (p.c / 2) + 4 * i;
   pdl_wait();
   const int4 meta = pl.meta[b];
   if (meta.x < 0 || h >= p.n_h) return;
-  const float sink = p.sink ? p.sink[h] * kLog2e : -INFINITY;
   auto slot = [&](int c) { return (long long)(2 * c + (c == meta.x ? meta.z : 0)); };
-  // one pass with a running maximum, 4 parts at a time
-  float M = sink, den = sink == -INFINITY ? 0.f : 1.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c0 = meta.x; c0 <= meta.y; c0 += 4) {
-    float2 ml[4];
-    float4 o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      ml[k] = make_float2(-INFINITY, 0.f);
-      if (c0 + k <= meta.y) {
-        ml[k] = pl.part_ml[slot(c0 + k) * p.n_h + h];
-        o[k] = pl.part_o[fp4_part(p, slot(c0 + k), q, i) + lane];
-      }
-    }
-    const float m = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), M);
-    if (m == -INFINITY) continue;
-    const float f = M == m ? 1.f : exp2f(M - m);   // an infinite sink takes all the weight
-    M = m;
-    den *= f;
-    acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (ml[k].x == -INFINITY) continue;     // a part without keys
-      const float e = exp2f(ml[k].x - M);
-      den += e * ml[k].y;
-      acc.x += e * o[k].x; acc.y += e * o[k].y; acc.z += e * o[k].z; acc.w += e * o[k].w;
-    }
-  }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
+  const float4 v = fp4_join(
+      p, h, meta.x, meta.y, [&](int c) { return pl.part_ml[slot(c) * p.n_h + h]; },
+      [&](int c) { return pl.part_o[fp4_part(p, slot(c), q, i) + lane]; });
+  float2 cs0 = make_float2(1.f, 0.f), cs1 = cs0;
   if (col >= p.c - p.rd) {
     const int pos = min(__ldg(p.positions + b), p.max_pos), k = (col - (p.c - p.rd)) / 2;
-    float s0, c0, s1, c1;
-    fp4_rope(p, pos, k, s0, c0);
-    fp4_rope(p, pos, k + 1, s1, c1);
-    acc = make_float4(acc.x * c0 + acc.y * s0, acc.y * c0 - acc.x * s0, acc.z * c1 + acc.w * s1, acc.w * c1 - acc.z * s1);
+    fp4_rope(p, pos, k, cs0.y, cs0.x);
+    fp4_rope(p, pos, k + 1, cs1.y, cs1.x);
   }
-  *reinterpret_cast<uint2 *>(p.o + ((long long)b * p.n_h + h) * p.c + col) =
-      make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+  fp4_rotate_store(p, b, h, col, v, cs0, cs1);
 }
 
 // CTAs of a call: the budget, no more than there can be tiles.  A part costs
@@ -772,6 +835,20 @@ int fp4_ctas(const AttendFp4Params &p, int ne, bool listed) {
   if (listed && p.B <= budget) return p.B * std::max(1, std::min(budget / p.B, tiles / least));
   return (int)std::max<long long>(1, std::min<long long>(budget, std::max<long long>(std::min(p.B, budget), (long long)p.B * tiles / least)));
 }
+// CTAs per sequence where a cluster takes each sequence and joins it through
+// shared memory: no parts in the workspace and no second launch, which cost as
+// much as about 4 tiles, but at most 8 CTAs, and a ragged batch waits for its
+// longest sequence (half of the most tiles is taken as the mean where only the
+// positions tell).  0 where runs over all sequences have that much less.
+int fp4_cluster(const AttendFp4Params &p, int ne, bool listed) {
+  const int sms = num_sms(), budget = p.max_ctas > 0 && p.max_ctas < sms ? p.max_ctas : sms;
+  const int nw = std::min(p.w, p.max_pos + 1), tiles = (nw + KT - 1) / KT + (ne + KT - 1) / KT;
+  int S = 1;
+  while (S < 8 && 2 * S <= tiles && (long long)p.B * 2 * S <= budget) S *= 2;
+  if (S == 1) return 0;
+  const int runs = (int)(((long long)p.B * tiles + fp4_ctas(p, ne, listed) - 1) / fp4_ctas(p, ne, listed));
+  return (tiles + S - 1) / S <= (listed ? runs : runs / 2) + 4 ? S : 0;
+}
 size_t fp4_align(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t fp4_part_bytes(const AttendFp4Params &p, size_t G) { return fp4_align(2 * G * ((p.n_h + 15) / 16 * 16) * p.c * 4); }
 
@@ -785,23 +862,49 @@ int launch_fp4(const AttendFp4Params &p, const Fp4Plan &pl, cudaStream_t s) {
     if (e != cudaSuccess) return fail(HCA_ERR_CUDA, "attend_fp4 smem attribute: %s", cudaGetErrorString(e));
     attr = true;
   }
-  return HCA_LAUNCH("attend_fp4", s, attend_fp4_kernel<C><<<pl.G, kThreads, Fp4Layout<C>::bytes, s>>>(p, pl));
+  LaunchScope ls("attend_fp4", s);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(pl.G, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Fp4Layout<C>::bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = pl.S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pl.S ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_fp4_kernel<C>, p, pl);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return fail(HCA_ERR_CUDA, "attend_fp4 launch: %s", cudaGetErrorString(e));
+  }
+  return ls.done();
 }
 
 }  // namespace
 
-// One CTA finishes every sequence itself and needs no workspace.
+// A cluster per sequence and one CTA for all need no workspace.
 size_t attend_fp4_workspace_bytes(const AttendFp4Params &p) {
-  const size_t G = (size_t)std::max(fp4_ctas(p, p.k, true), fp4_ctas(p, (p.max_pos + 1) / p.m, false));   // listed or not
-  return G == 1 ? 0 : fp4_part_bytes(p, G) + fp4_align(2 * G * p.n_h * 8) + fp4_align((size_t)p.B * 16);
+  size_t most = 0;
+  for (const bool listed : {true, false}) {
+    const int ne = listed ? p.k : (p.max_pos + 1) / p.m;
+    const size_t G = (size_t)fp4_ctas(p, ne, listed);
+    if (G == 1 || fp4_cluster(p, ne, listed)) continue;
+    most = std::max(most, fp4_part_bytes(p, G) + fp4_align(2 * G * p.n_h * 8) + fp4_align((size_t)p.B * 16));
+  }
+  return most;
 }
 
 int run_attend_fp4(const AttendFp4Params &p, void *ws, size_t, cudaStream_t s) {
   Fp4Plan pl{};
-  pl.G = p.idx ? fp4_ctas(p, p.k, true) : fp4_ctas(p, (p.max_pos + 1) / p.m, false);
+  const bool listed = p.idx != nullptr;
+  const int ne = listed ? p.k : (p.max_pos + 1) / p.m;
+  pl.S = fp4_cluster(p, ne, listed);
+  pl.G = pl.S ? p.B * pl.S : fp4_ctas(p, ne, listed);
   pl.fd_m = make_fastdiv((uint32_t)p.m);
   pl.fd_cap = make_fastdiv((uint32_t)std::max(p.cap, 1));
-  if (pl.G > 1) {
+  if (pl.G > 1 && !pl.S) {
     char *w = static_cast<char *>(ws);
     pl.part_o = reinterpret_cast<float4 *>(w);
     w += fp4_part_bytes(p, pl.G);
@@ -810,7 +913,7 @@ int run_attend_fp4(const AttendFp4Params &p, void *ws, size_t, cudaStream_t s) {
     pl.meta = reinterpret_cast<int4 *>(w);
   }
   const int rc = p.c == 128 ? launch_fp4<128>(p, pl, s) : p.c == 256 ? launch_fp4<256>(p, pl, s) : launch_fp4<512>(p, pl, s);
-  if (rc || pl.G == 1) return rc;
+  if (rc || pl.G == 1 || pl.S) return rc;
   LaunchScope ls("attend_fp4_combine", s);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.B, p.c / 32, (p.n_h + 15) / 16);
