@@ -15,8 +15,9 @@
 //
 // Per tile (tcgen05, the sequence's n_h <= 64 heads as the MMA's M = 64):
 //   8 loader warps   codes of the next tile on their way into shared memory
-//                    (cp.async, every thread its own parts: no barrier) while
-//                    this one's become bf16 (exact: two significant bits and a
+//                    (cp.async, every thread its own parts: no barrier; asked
+//                    for before this tile's are converted) while this one's
+//                    become bf16 (exact: two significant bits and a
 //                    power of two) in a 128B-swizzled tile that serves as K
 //                    (K-major) and V (MN-major); RoPE channels and window rows
 //                    are copied into the tile, skipped keys are zero rows
@@ -103,7 +104,7 @@ struct Fp4Layout {
 };
 
 struct Fp4Bars {
-  uint64_t q_full, q_empty, o_empty, kv_full[8], kv_empty[8], s_full[SP], s_empty[SP], p_full[SP], pv_done[SP];
+  uint64_t q_full, q_empty, o_empty, all_done, kv_full[8], kv_empty[8], s_full[SP], s_empty[SP], p_full[SP], pv_done[SP];
   uint32_t tmem;
 };
 
@@ -254,34 +255,42 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
       }
       cp_async_arrive_noinc(full);         // before the next tile's copies
     }
-    // ---- its codes, and in their place those of t1
-    if (nu && t1.kind == 1) cp_async4(rawe, rp1 + (t1.cnt ? eoff : 0), t1.cnt ? 4 : 0);
-#pragma unroll 1
-    for (int i = 0; i < nu; ++i, ex >>= 8) {
-      uint4 c = make_uint4(0, 0, 0, 0);
-      if (t0.kind == 1) c = *reinterpret_cast<const uint4 *>(smem + L::raw_off + i * 4096 + pt * 16);
-      if (t1.kind == 1) cp_async16(rawc + i * 4096, rp1 + (t1.cnt ? 16 * (u0 + i) : 0), t1.cnt ? 16 : 0);
-      if (t0.kind != 1) continue;
-      const int u = u0 + i;                // channels 32 u .. 32 u + 31
-      const float sc = pow2f(max((int)(ex & 255u), 1) - 127);   // byte 0: all codes are zero
-      const uint32_t wd[4] = {c.x, c.y, c.z, c.w};
-      uint8_t *dst = tile + (u / 2) * kTileBytes;
+    // ---- its codes, and in their place those of t1, asked for before this tile's are converted
+    uint4 code[4];
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t f[4], o[4];
-        e2m1x8_f16(wd[h], f);
+    for (int i = 0; i < 4; ++i)
+      if (i < nu && t0.kind == 1) code[i] = *reinterpret_cast<const uint4 *>(smem + L::raw_off + i * 4096 + pt * 16);
+    if (t1.kind == 1) {
+      if (nu) cp_async4(rawe, rp1 + (t1.cnt ? eoff : 0), t1.cnt ? 4 : 0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f[q]));
-          o[q] = pack_bf16x2(v.x * sc, v.y * sc);
+      for (int i = 0; i < 4; ++i)
+        if (i < nu) cp_async16(rawc + i * 4096, rp1 + (t1.cnt ? 16 * (u0 + i) : 0), t1.cnt ? 16 : 0);
+    }
+    if (t0.kind == 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i, ex >>= 8) {
+        if (i >= nu) break;
+        const int u = u0 + i;                // channels 32 u .. 32 u + 31
+        const float sc = pow2f(max((int)(ex & 255u), 1) - 127);   // byte 0: all codes are zero
+        const uint32_t wd[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+        uint8_t *dst = tile + (u / 2) * kTileBytes;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t f[4], o[4];
+          e2m1x8_f16(wd[h], f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f[q]));
+            o[q] = pack_bf16x2(v.x * sc, v.y * sc);
+          }
+          *reinterpret_cast<uint4 *>(dst + sw128_off(kk, (u & 1) * 4 + h)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *reinterpret_cast<uint4 *>(dst + sw128_off(kk, (u & 1) * 4 + h)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
     if (t0.kind) {
       fence_proxy_async();      // the tensor cores read the tile through the async proxy
-      mbar_arrive(full);
-      if (pt == 0) mbar_arrive(full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
       if (++st == L::NS) {
         st = 0;
         ph ^= 1;
@@ -359,6 +368,8 @@ __device__ __forceinline__ void fp4_mma(const AttendFp4Params &p, const Fp4Plan 
     }
     if (ok) issue_pv(w.cnt == 1);
   }
+  if (ok && elect_one()) umma_commit(bar(bars->all_done));
+  __syncwarp();
 }
 
 // sin and cos of position pos for pair i; the angle is reduced in double to
@@ -368,6 +379,27 @@ __device__ __forceinline__ void fp4_rope(const AttendFp4Params &p, int pos, int 
   double a = (double)pos * f;
   a -= 6.283185307179586476925286766559 * rint(a * 0.15915494309189533576888376337251);
   __sincosf((float)a, &sn, &cs);
+}
+
+// Part `slot`'s sums of heads 16 q .. from tensor memory, 32 columns of either
+// half at a time, every step-th of these from the first-th on.  A warp reads
+// the lanes 32 (warp % 4) .., so q is warp % 4.
+template <int C>
+__device__ __forceinline__ void fp4_part_store(const AttendFp4Params &p, float4 *part, long long slot, uint32_t tmem, int q,
+                                               int first, int step) {
+  if (16 * q >= p.n_h) return;
+  float4 *dst = part + fp4_part(p, slot, q, 8 * first) + (threadIdx.x & 31);
+#pragma unroll 1
+  for (int c0 = 32 * first; c0 < C / 2; c0 += 32 * step, dst += 256 * step) {
+    uint32_t ov[32];
+    tmem_ld_16x32bx2_x16<C / 2>(tmem + ((uint32_t)(q * 32) << 16) + c0, *reinterpret_cast<uint32_t(*)[16]>(&ov[0]));
+    tmem_ld_16x32bx2_x16<C / 2>(tmem + ((uint32_t)(q * 32) << 16) + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&ov[16]));
+    tmem_ld_wait();
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      dst[32 * x] = make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]),
+                                __uint_as_float(ov[4 * x + 3]));
+  }
 }
 
 // ---------------------------------------------------------------- softmax + epilogue
@@ -388,17 +420,42 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
   uint32_t kph = 0;
   int before = run.before;
 
-  auto write_q = [&](int b) {             // Q into tensor memory
+  // Q into tensor memory, 64 channels of either half at a time: read 8 lanes to
+  // 128 contiguous bytes and turned through this warp's 4 KB of the P buffers
+  // (a lane to a row of its own touches 32 lines per load: 64 x 512 took 9000
+  // cycles).  No P V may be reading the buffers.
+  auto write_q = [&](int b) {
     tc_fence_after();
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.q + ((long long)b * p.n_h + (live ? r : 0)) * C + half * (C / 2));
+    const int sg = lane >> 3, ch = lane & 7;        // of 4 segments (head, half) per load; 16-byte chunk
+    uint8_t *turn = smem + L::p_off + warp * 4096;
+    const __nv_bfloat16 *src = p.q + (long long)b * p.n_h * C + 8 * ch;
     const uint32_t tq = tmem + lane_S + L::q_col;
-#pragma unroll 1
-    for (int b0 = 0; b0 < C / 16; b0 += 8) {
-      uint4 v[8];
+    auto load = [&](int c0, uint4 (&v)[8]) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x) v[x] = live ? __ldg(src + b0 + x) : make_uint4(0, 0, 0, 0);
-      tmem_st_16x32bx2_x16<C / 4>(tq + 4 * b0, *reinterpret_cast<const uint32_t(*)[16]>(&v[0]));
-      tmem_st_16x32bx2_x16<C / 4>(tq + 4 * b0 + 16, *reinterpret_cast<const uint32_t(*)[16]>(&v[4]));
+      for (int x = 0; x < 8; ++x) {
+        const int seg = 4 * x + sg, row = warp * 16 + (seg & 15);
+        v[x] = row < p.n_h ? __ldg(reinterpret_cast<const uint4 *>(src + (long long)row * C + (seg >> 4) * (C / 2) + c0))
+                           : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto turned = [&](int c0, uint4 (&v)[8]) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int seg = 4 * x + sg;
+        *reinterpret_cast<uint4 *>(turn + seg * 128 + ((ch ^ (seg & 7)) << 4)) = v[x];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] = *reinterpret_cast<const uint4 *>(turn + lane * 128 + ((x ^ (lane & 7)) << 4));
+      __syncwarp();
+      tmem_st_16x32bx2_x16<C / 4>(tq + c0 / 2, *reinterpret_cast<const uint32_t(*)[16]>(&v[0]));
+      tmem_st_16x32bx2_x16<C / 4>(tq + c0 / 2 + 16, *reinterpret_cast<const uint32_t(*)[16]>(&v[4]));
+    };
+    uint4 v0[8];
+#pragma unroll 1
+    for (int c0 = 0; c0 < C / 2; c0 += 64) {
+      load(c0, v0);
+      turned(c0, v0);
     }
     tmem_st_wait();
     tc_fence_before();
@@ -408,6 +465,14 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
   Fp4Walk w = fp4_walk(run);
   bool more = fp4_next(p, pl, run, w);
   if (more) write_q(w.b);
+  // in a cluster the rotation's table is worked out before it is needed
+  float2 turns[2] = {};
+  if (pl.S) {
+    const int pos = min(__ldg(p.positions + run.b0), p.max_pos);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if ((int)threadIdx.x + 128 * x < p.rd / 2) fp4_rope(p, pos, threadIdx.x + 128 * x, turns[x].y, turns[x].x);
+  }
   for (; more; ++npiece) {
     float m_used = -INFINITY, l = 0.f;    // running maximum (log2 units; -inf until a key is seen), sum of this half
     for (int j = 0; j < w.cnt; ++j, ++g) {
@@ -485,11 +550,16 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
       if (lane == 0) mbar_arrive(bar(bars->p_full[st]));
     }
 
-    // the next piece's Q before this one's epilogue, so that its first S need not wait for that
+    // the last P V, then the next piece's Q before this one's epilogue, so that its first S need not wait for that
+    {
+      const uint32_t gl = g - 1;
+      if (!mbar_wait_fast(bar(bars->pv_done[gl % SP]), (gl / SP) & 1, p.status)) return;
+    }
     Fp4Walk wn = w;
     more = fp4_next(p, pl, run, wn);
     if (more) {
       if (!mbar_wait_fast(bar(bars->q_empty), npiece & 1, p.status)) return;
+      asm volatile("bar.sync 1, 128;" ::: "memory");   // all warps are past the P V that reads all of P
       write_q(wn.b);
     }
     // ---- epilogue
@@ -501,13 +571,10 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
       pl.meta[w.b] = whole ? make_int4(-1, 0, 0, 0)
                            : make_int4(blockIdx.x, fp4_cta_of(run, last), before == run.before ? 0 : 1, 0);
     }
-    {
-      const uint32_t gl = g - 1;
-      if (!mbar_wait_fast(bar(bars->pv_done[gl % SP]), (gl / SP) & 1, p.status)) return;
-    }
     tc_fence_after();
     if (whole) {
-      // the rotation's table, where P was: the last P V has completed
+      // the rotation's table, where P was (and other warps' Q on its way)
+      if (more) asm volatile("bar.sync 1, 128;" ::: "memory");
       for (int i = threadIdx.x; i < p.rd / 2; i += 128) {
         float sn, cs;
         fp4_rope(p, w.k.pos, i, sn, cs);
@@ -523,20 +590,8 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
       // key tiles were
       float2 *ml = pl.S ? reinterpret_cast<float2 *>(smem + L::p_off) : pl.part_ml + slot * p.n_h;
       if (live && half == 0) ml[r] = make_float2(m_used, ltot);
-      if (warp * 16 < p.n_h) {
-        float4 *dst = (pl.S ? reinterpret_cast<float4 *>(smem) + fp4_part(p, 0, warp, 0) : pl.part_o + fp4_part(p, slot, warp, 0)) + lane;
-#pragma unroll 1
-        for (int c0 = 0; c0 < C / 2; c0 += 32, dst += 256) {
-          uint32_t ov[32];
-          tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0, *reinterpret_cast<uint32_t(*)[16]>(&ov[0]));
-          tmem_ld_16x32bx2_x16<C / 2>(tmem + lane_O + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(&ov[16]));
-          tmem_ld_wait();
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            dst[32 * x] = make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]),
-                                      __uint_as_float(ov[4 * x + 3]));
-        }
-      }
+      if (pl.S) fp4_part_store<C>(p, reinterpret_cast<float4 *>(smem), 0, tmem, warp, 0, 3);   // the loaders store the rest
+      else fp4_part_store<C>(p, pl.part_o, slot, tmem, warp, 0, 1);
     } else {
       uint4 *dst = reinterpret_cast<uint4 *>(p.o + ((long long)w.b * p.n_h + r) * C + half * (C / 2));
 #pragma unroll 1
@@ -573,6 +628,14 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
     if (lane == 0) mbar_arrive(bar(bars->o_empty));
     before += w.cnt;
     w = wn;
+  }
+  if (pl.S) {
+    if (run.n == 0 && threadIdx.x < 64)   // a part without keys
+      reinterpret_cast<float2 *>(smem + L::p_off)[threadIdx.x] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if ((int)threadIdx.x + 128 * x < p.rd / 2)
+        reinterpret_cast<float2 *>(smem + L::p_off + 1024)[threadIdx.x + 128 * x] = turns[x];
   }
 }
 
@@ -621,20 +684,50 @@ __device__ __forceinline__ void fp4_rotate_store(const AttendFp4Params &p, int b
 }
 
 // A cluster's sequence: its CTAs have their parts in shared memory, and each
-// joins a share of the columns.
+// joins a share of the columns, first the heads' weights of the parts.
 template <int C>
 __device__ __forceinline__ void fp4_cluster_join(const AttendFp4Params &p, const Fp4Plan &pl, int b, uint8_t *smem) {
   using L = Fp4Layout<C>;
   const int lane = threadIdx.x & 31, per = C / 8 / pl.S, rank = blockIdx.x % pl.S;
   const float2 *rope = reinterpret_cast<const float2 *>(smem + L::p_off + 1024);
+  float *wts = reinterpret_cast<float *>(smem + L::p_off + 4096);    // [64][8]
   const uint32_t sbase = smem_u32(smem);
+  if ((int)threadIdx.x < p.n_h) {
+    const int h = threadIdx.x;
+    const float sink = p.sink ? p.sink[h] * kLog2e : -INFINITY;
+    float2 ml[8];
+    float M = sink;
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      ml[s] = s < pl.S ? ld_dsmem_f32x2(cluster_map(sbase + L::p_off + 8 * h, s)) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) M = fmaxf(M, ml[s].x);
+    float den = sink == -INFINITY ? 0.f : sink == M ? 1.f : exp2f(sink - M);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      ml[s].x = ml[s].x == -INFINITY ? 0.f : exp2f(ml[s].x - M);     // 0: a part without keys
+      den += ml[s].x * ml[s].y;
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) wts[8 * h + s] = ml[s].x * inv;
+  }
+  __syncthreads();
+#pragma unroll 1
   for (int pair = threadIdx.x >> 5; pair < (p.n_h + 15) / 16 * per; pair += kThreads / 32) {
     const int q = pair / per, i = rank * per + pair % per, h = 16 * q + (lane & 15), col = (lane >> 4) * (C / 2) + 4 * i;
     if (h >= p.n_h) continue;
     const uint32_t off = (uint32_t)(fp4_part(p, 0, q, i) + lane) * 16u;
-    const float4 v = fp4_join(
-        p, h, 0, pl.S - 1, [&](int s) { return ld_dsmem_f32x2(cluster_map(sbase + L::p_off + 8 * h, s)); },
-        [&](int s) { return ld_dsmem_f32x4(cluster_map(sbase + off, s)); });
+    float4 o[8], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s < pl.S) o[s] = ld_dsmem_f32x4(cluster_map(sbase + off, s));
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float w = wts[8 * h + s];
+      if (w == 0.f) continue;        // its sums may be anything
+      v.x += w * o[s].x; v.y += w * o[s].y; v.z += w * o[s].z; v.w += w * o[s].w;
+    }
     const int k = (col - (C - p.rd)) / 2;
     const bool rot = col >= C - p.rd;
     fp4_rotate_store(p, b, h, col, v, rot ? rope[k] : make_float2(1.f, 0.f), rot ? rope[k + 1] : make_float2(1.f, 0.f));
@@ -653,8 +746,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
     mbar_init(bar(bars->q_full), 4);
     mbar_init(bar(bars->q_empty), 1);
     mbar_init(bar(bars->o_empty), 4);
+    mbar_init(bar(bars->all_done), 1);
     for (int i = 0; i < L::NS; ++i) {
-      mbar_init(bar(bars->kv_full[i]), 2 * kLoadWarps * 32 + 1);   // every thread's copies and stores, and the mask
+      mbar_init(bar(bars->kv_full[i]), kLoadWarps * 33);   // every thread's copies, every warp's stores
       mbar_init(bar(bars->kv_empty[i]), 1);
     }
     for (int i = 0; i < SP; ++i) {
@@ -766,19 +860,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
 
   if (warp >= kLoad0) {
     fp4_load<C>(p, pl, run, smem, bars);
+    // a cluster's CTA has one piece; its sums are there once all MMAs have run (pv_done's phases are not followed here)
+    if (pl.S && run.n > 0 && mbar_wait_fast(bar(bars->all_done), 0, p.status)) {
+      tc_fence_after();
+      __syncwarp();
+      fp4_part_store<C>(p, reinterpret_cast<float4 *>(smem), 0, tmem, warp & 3, 1 + (warp - kLoad0) / 4, 3);
+    }
   } else if (warp == kMmaWarp) {
     fp4_mma<C>(p, pl, run, smem_u32(smem), bars, tmem);
   } else {
     fp4_softmax<C>(p, pl, run, smem, bars, tmem);
-    if (pl.S) {
-      if (run.n == 0 && threadIdx.x < 64)   // a part without keys
-        reinterpret_cast<float2 *>(smem + L::p_off)[threadIdx.x] = make_float2(-INFINITY, 0.f);
-      for (int i = threadIdx.x; i < p.rd / 2; i += 128) {
-        float sn, cs;
-        fp4_rope(p, min(__ldg(p.positions + run.b0), p.max_pos), i, sn, cs);
-        reinterpret_cast<float2 *>(smem + L::p_off + 1024)[i] = make_float2(cs, sn);
-      }
-    }
     // sequences without keys: zeros
     for (int b = pl.S ? p.B : (int)blockIdx.x; b < p.B; b += pl.G) {
       if (fp4_keys(p, pl, b).nt) continue;
