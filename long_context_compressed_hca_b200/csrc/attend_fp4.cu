@@ -6,12 +6,16 @@
 // are visible); z_j = scale q_h . row_j; o_h = sum_j e^{z_j} row_j /
 // (sum_j e^{z_j} + e^{sink_h}); the last rd dims of o_h rotated by -pos.
 //
-// Keys are taken 64 at a time, a sequence's window tiles last.  The tiles of
-// all sequences form one list, and every CTA takes an equal run of it, so that
-// ragged lengths cost nothing and few sequences still fill the GPU; the runs
-// follow from the positions on the device, which each CTA sums up itself.  A
-// sequence inside one run is finished there; one that was cut leaves
-// unnormalised fp32 parts, which fp4_combine_kernel joins in their order.
+// Keys are taken 64 at a time, a sequence's window tiles last.  Two ways to
+// spread the tiles (fp4_cluster chooses):
+//   runs      the tiles of all sequences form one list, and every CTA takes an
+//             equal run of it, so that ragged lengths cost nothing; the runs
+//             follow from the positions on the device, which each CTA sums up
+//             itself.  A sequence inside one run is finished there; one that
+//             was cut leaves unnormalised fp32 parts in the workspace, which
+//             fp4_combine_kernel joins in their order.
+//   clusters  2, 4 or 8 CTAs share a sequence's tiles equally and join their
+//             parts through distributed shared memory (fp4_cluster_join).
 //
 // Per tile (tcgen05, the sequence's n_h <= 64 heads as the MMA's M = 64):
 //   8 loader warps   codes of the next tile on their way into shared memory
@@ -26,10 +30,14 @@
 //   4 softmax warps  S from tensor memory, running maximum moved only when it
 //                    grows by more than 2^8, P in bf16 (its rounding, 2^-8 of
 //                    p, is that of the bf16 output; sums and statistics fp32)
-// Bound: M = 64 uses half the tensor pipe, 2048 cycles per tile at c = 512,
-// against 900 for the conversion and 64 x 368 bytes of HBM (1000 cycles at an
-// SM's share).  With few tiles per CTA the fixed parts (first loads, fill of
-// the pipeline, joining) are most of the time.
+// Bound: a tile takes 3300 cycles of a CTA at c = 512 (32 sequences of 16384
+// entries: 123 us).  M = 64 uses half the tensor pipe, 2460 cycles of MMAs; the
+// loader warps need 3100, about the same with the conversion by other
+// instructions (byte lookups in the integer pipe, a mixture of both) or ordered
+// otherwise, and wait for 300.  64 x 368 bytes of HBM are 1000 cycles of an
+// SM's share.  With few tiles per CTA the fixed parts (entry, page and code
+// loads one after another, Q, the join) are most of the time: 5 tiles a
+// sequence and CTA pair took 24 us as runs, 2 or 3 a CTA 19 in clusters.
 #include <algorithm>
 
 #include "internal.h"
@@ -917,8 +925,8 @@ __global__ void __launch_bounds__(128) fp4_combine_kernel(AttendFp4Params p, Fp4
 // its n_h x c sums written and read again, so a CTA gets at least as many tiles
 // as keep that small beside them (64 x 512: 4), and listed entries, whose count
 // is known here, are cut into equal parts of each sequence: 32 sequences of 10
-// tiles at 64 x 512 take 27.5 us on 64 CTAs, 31 on 32 (whole sequences), 96 and
-// 148; one sequence of 10 tiles at 16 x 128 takes 11.2 us on 10 CTAs, 13.2 on 3.
+// tiles at 64 x 512, as runs, took 27.5 us on 64 CTAs, 31 on 32 (whole
+// sequences), 96 and 148.
 int fp4_ctas(const AttendFp4Params &p, int ne, bool listed) {
   const int sms = num_sms(), budget = p.max_ctas > 0 && p.max_ctas < sms ? p.max_ctas : sms;
   const int nw = std::min(p.w, p.max_pos + 1), tiles = (nw + KT - 1) / KT + (ne + KT - 1) / KT;
@@ -930,7 +938,9 @@ int fp4_ctas(const AttendFp4Params &p, int ne, bool listed) {
 // shared memory: no parts in the workspace and no second launch, which cost as
 // much as about 4 tiles, but at most 8 CTAs, and a ragged batch waits for its
 // longest sequence (half of the most tiles is taken as the mean where only the
-// positions tell).  0 where runs over all sequences have that much less.
+// positions tell).  0 where runs over all sequences have that much less.  32
+// sequences of 10 tiles at 64 x 512: 19.3 us in clusters of 4, 24.3 as runs;
+// one of 10 tiles at 16 x 128: 9.3 us in a cluster of 8, 10.0 as runs.
 int fp4_cluster(const AttendFp4Params &p, int ne, bool listed) {
   const int sms = num_sms(), budget = p.max_ctas > 0 && p.max_ctas < sms ? p.max_ctas : sms;
   const int nw = std::min(p.w, p.max_pos + 1), tiles = (nw + KT - 1) / KT + (ne + KT - 1) / KT;
