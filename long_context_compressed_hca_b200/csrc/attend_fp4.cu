@@ -30,8 +30,8 @@
 //   4 softmax warps  S from tensor memory, running maximum moved only when it
 //                    grows by more than 2^8, P in bf16 (its rounding, 2^-8 of
 //                    p, is that of the bf16 output; sums and statistics fp32)
-// Bound: a tile takes 3300 cycles of a CTA at c = 512 (32 sequences of 16384
-// entries: 123 us).  M = 64 uses half the tensor pipe, 2460 cycles of MMAs; the
+// Bound: a tile takes 3250 cycles of a CTA at c = 512 (32 sequences of 16384
+// entries: 120 us).  M = 64 uses half the tensor pipe, 2460 cycles of MMAs; the
 // loader warps need 3100, about the same with the conversion by other
 // instructions (byte lookups in the integer pipe, a mixture of both) or ordered
 // otherwise, and wait for 300.  64 x 368 bytes of HBM are 1000 cycles of an
@@ -176,6 +176,8 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
   const int per = units <= 4 ? 1 : units <= 8 ? 2 : 4;          // units of this thread: u0 .. u0 + nu - 1
   const int u0 = grp * per, nu = max(0, min(per, units - u0));
   const int eoff = nq / 2 + 2 * p.rd + (u0 & ~3), esh = 8 * (u0 & 3);
+  // RoPE chunks go to the threads with fewer than `per` units, where there are any
+  const int busy = units / per, rfirst = busy == 4 ? grp : grp < busy ? rch : grp - busy, rstep = busy == 4 ? 4 : 4 - busy;
   const uint32_t sbase = smem_u32(smem), rawc = sbase + L::raw_off + pt * 16, rawe = sbase + L::raw_off + 4 * 4096 + pt * 4;
   const unsigned char *none = reinterpret_cast<const unsigned char *>(p.q);   // an address for copies of nothing
 
@@ -254,7 +256,7 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
         }
       } else {
         cp_async_wait_all();               // this thread's codes are here
-        for (int ch = grp; ch < rch; ch += 4)
+        for (int ch = rfirst; ch < rch; ch += rstep)
           cp_async16(tdst + ((nq / 8 + ch) / 8) * kTileBytes + sw128_off(kk, (nq / 8 + ch) % 8),
                      rp0 + (t0.cnt ? nq / 2 + 16 * ch : 0), t0.cnt ? 16 : 0);
         const uint32_t m = __ballot_sync(0xffffffffu, t0.cnt);
