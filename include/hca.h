@@ -520,7 +520,7 @@ int hca_w4_linear(const hca_w4_desc *d, const void *x, const float *x_scale, con
  * amax_group / top / row_scale; code = nearest (ties to even; saturating at
  * +-top) of w / (row_scale * scale): each operation rounded to fp32, 0 where
  * the divisor is 0.  Zero is stored as code 0.  Also clears the scales' padding
- * columns.  Weights must be finite. */
+ * columns.  Weights must be finite.  The four buffers may not overlap. */
 int hca_w4_quantize(const hca_w4_desc *d, const void *w, hca_dtype w_dtype, void *codes, void *scales,
                     float *row_scale, hca_stream_t stream);
 
@@ -540,7 +540,8 @@ int hca_w4_quantize(const hca_w4_desc *d, const void *w, hca_dtype w_dtype, void
  * r).  quant skips a row whose slot lies outside [0, records), so a slot of -1
  * drops the row; the other slots of one call must be distinct (of two rows with
  * one slot the record holds a mixture).  dequant writes a zero row for a slot
- * outside [0, records).  rows = 0 is a no-op. */
+ * outside [0, records).  rows = 0 is a no-op.  What is written may not overlap
+ * an input. */
 size_t hca_kv_fp4_row_bytes(int c, int rd);   /* 0 when (c, rd) is unsupported */
 int hca_kv_quant_fp4(const void *x, hca_dtype x_dtype, long long rows, int c, int rd, void *out, long long records,
                      const long long *slots, hca_stream_t stream);

@@ -279,9 +279,11 @@ PyObject *attend_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
                   sh[1] = {d->n_h}, sb[1] = {B}, sp[2] = {B, cache->max_pages};
     const void *pq = take("q", q, sq, kBF16, dev), *po = take("o", a[10], sq, kBF16, dev);
     int64_t nrec;
-    records("cache rows", rows, d->c, d->rd, dev, &nrec);
-    if (a[4] != Py_None) take("pages", a[4], sp, kI32, dev);
-    else if (rows.size(0) != B)
+    const void *pr = records("cache rows", rows, d->c, d->rd, dev, &nrec);
+    const void *pg = take_or_null("pages", a[4], sp, kI32, dev);
+    if (pr != cache->rows || pg != static_cast<const void *>(cache->pages))
+      bad("the cache's tensors have moved since fp4_cache made it");
+    if (a[4] == Py_None && rows.size(0) != B)
       bad("the cache has " + std::to_string(rows.size(0)) + " sequences, expected " + std::to_string(B));
     const void *pi = take_or_null("idx", a[5], si, kI32, dev);
     const void *pk = take_or_null("kv_win", a[6], sw, kBF16, dev);

@@ -142,6 +142,13 @@ int hca_w4_quantize(const hca_w4_desc *d, const void *w, hca_dtype w_dtype, void
   REQUIRE(w && codes && scales && row_scale, "w, codes, scales and row_scale must be non-null");
   REQUIRE(aligned16(w) && aligned16(codes) && aligned16(scales) && aligned16(row_scale),
           "pointers must be 16-byte aligned");
+  {
+    const size_t gn = (size_t)d->groups * d->N;
+    const struct { const void *p; size_t n; } b[4] = {{w, gn * d->K * esize(w_dtype)}, {codes, gn * (d->K / 2)},
+                                                      {scales, (size_t)d->groups * (d->K / p.G) * p.ldn}, {row_scale, gn * 4}};
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < i; ++j) REQUIRE(!overlap(b[i].p, b[i].n, b[j].p, b[j].n), "w, codes, scales and row_scale overlap");
+  }
   return launch_w4_quantize(w, w_dtype, p, codes, scales, row_scale, static_cast<cudaStream_t>(stream));
 }
 
@@ -160,6 +167,7 @@ int hca_kv_quant_fp4(const void *x, hca_dtype x_dtype, long long rows, int c, in
   REQUIRE((reinterpret_cast<uintptr_t>(slots) & 7u) == 0, "slots must be 8-byte aligned");
   REQUIRE(!overlap(out, (size_t)records * kv_fp4_row_bytes(c, rd), x, (size_t)rows * c * esize(x_dtype)),
           "the records overlap x");
+  REQUIRE(!overlap(out, (size_t)records * kv_fp4_row_bytes(c, rd), slots, (size_t)rows * 8), "the records overlap slots");
   return launch_kv_quant_fp4(x, x_dtype, rows, c, rd, out, records, slots, static_cast<cudaStream_t>(stream));
 }
 
@@ -174,6 +182,7 @@ int hca_kv_dequant_fp4(const void *in, long long records, const long long *slots
   REQUIRE((reinterpret_cast<uintptr_t>(slots) & 7u) == 0, "slots must be 8-byte aligned");
   REQUIRE(!overlap(in, (size_t)records * kv_fp4_row_bytes(c, rd), out, (size_t)rows * c * 2),
           "out overlaps the records");
+  REQUIRE(!overlap(out, (size_t)rows * c * 2, slots, (size_t)rows * 8), "out overlaps slots");
   return launch_kv_dequant_fp4(in, records, slots, rows, c, rd, out, static_cast<cudaStream_t>(stream));
 }
 

@@ -45,6 +45,11 @@ def test_device_tensors_of_a_wrong_kind_are_refused(cuda):
     s = _attn_case(2, 16, 128, 64, 8, 4, [30, 20])
     s["store"] = s["store"][:1]
     _refused("1 sequences, expected 2", lambda: _attn_call(s))
+    s = _attn_case(2, 16, 128, 64, 8, 4, [30, 20])
+    cache = hb.fp4_cache(s["store"], s["cap"])
+    cache.rows = s["store"].clone()              # the handle's addresses are the old tensor's
+    da, o = hb.attn_desc(2, 16, 128, 64, 8, 4, dtype=hb.HCA_BF16), torch.empty_like(s["q"])
+    _refused("have moved", lambda: hb.attend_fp4(da, s["q"], cache, None, s["win"], s["sink"], s["positions"], 30, o, ws))
     assert torch.equal(x, _n((4, 512), 1, 1, BF16)) and hb.device_status() == hb.HCA_OK
 
 
