@@ -378,7 +378,7 @@ __device__ __forceinline__ void fp4_mma(const AttendFp4Params &p, const Fp4Plan 
     }
     if (ok) issue_pv(w.cnt == 1);
   }
-  if (ok && elect_one()) umma_commit(bar(bars->all_done));
+  if (ok && pl.S && run.n > 0 && elect_one()) umma_commit(bar(bars->all_done));   // the loaders wait for it
   __syncwarp();
 }
 
