@@ -22,32 +22,40 @@ constexpr int kBlk = 256;        // channels of one work unit (one pipeline stag
 constexpr int kTileN = 128;      // outputs of one tile: the MMA's M
 
 // ---------------------------------------------------------------- codes
-// Eight codes as f16 pairs, times the scale s2 (INT4: plus t2).  E2M1 pairs
-// are neighbouring channels.  INT4 pairs are channels (i, i + 4), which the
-// masks leave in place, and x is laid out alike (pair4): u = code + 8 under
-// the exponent of 1024 is the f16 value 1024 + u, and (1024 + u) s - 1032 s by
-// one fused multiply-add is (u - 8) s, exact since 1032 s has at most 11
+// Eight codes as f16 pairs, times the scale.  E2M1 pairs are neighbouring
+// channels.  INT4 pairs are channels (i, i + 4), which the masks leave in
+// place, and x is laid out alike: with u = code + 8 in the low bits under the
+// exponent of 1024 the f16 value is 1024 + u, four bits higher 1024 + 16 u, so
+// that one shift serves four pairs (the integer pipe bounds the decoding);
+// (1024 + u) s - 1032 s and (1024 + 16 u) s / 16 - 72 s by one fused
+// multiply-add are (u - 8) s, exact since 1032 s and 72 s have at most 11
 // significant bits.  s is the scale times 2^-9 there so that 1032 s stays in
-// range; the 2^9 is in the epilogue's factor.
+// range, and s / 16 is a multiple of 2^-22; the 2^9 is in the epilogue's factor.
 template <int CODE>
-__device__ __forceinline__ void w4_scale(uint32_t byte, uint32_t &s2, uint32_t &t2) {
-  s2 = e4m3_f16x2_dup(byte);
-  t2 = 0u;
-  if constexpr (CODE == HCA_W4_INT4) {
-    s2 = hmul2_u32(s2, 0x18001800u);        // 2^-9
-    t2 = hmul2_u32(s2, 0xE408E408u);        // -1032
+struct W4Scale {
+  uint32_t s, t, s16, t16;       // INT4: t = -1032 s, s / 16, t16 = -72 s
+  __device__ __forceinline__ explicit W4Scale(uint32_t byte) : s(e4m3_f16x2_dup(byte)), t(0u), s16(0u), t16(0u) {
+    if constexpr (CODE == HCA_W4_INT4) {
+      s = hmul2_u32(s, 0x18001800u);          // 2^-9
+      t = hmul2_u32(s, 0xE408E408u);          // -1032
+      s16 = hmul2_u32(s, 0x2C002C00u);        // 1/16
+      t16 = hmul2_u32(s, 0xD480D480u);        // -72
+    }
   }
-}
+};
 template <int CODE>
-__device__ __forceinline__ void w4_decode8(uint32_t w, uint32_t s2, uint32_t t2, uint32_t *r) {
+__device__ __forceinline__ void w4_decode8(uint32_t w, const W4Scale<CODE> &sc, uint32_t *r) {
   if constexpr (CODE == HCA_W4_E2M1) {
     uint32_t f[4];
     e2m1x8_f16(w, f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = hmul2_u32(f[j], s2);
+    for (int j = 0; j < 4; ++j) r[j] = hmul2_u32(f[j], sc.s);
   } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = hfma2_u32(((w >> (4 * j)) & 0x000F000Fu) ^ 0x64086408u, s2, t2);
+    const uint32_t h = w >> 8;
+    r[0] = hfma2_u32((w & 0x000F000Fu) ^ 0x64086408u, sc.s, sc.t);
+    r[1] = hfma2_u32((w & 0x00F000F0u) ^ 0x64806480u, sc.s16, sc.t16);
+    r[2] = hfma2_u32((h & 0x000F000Fu) ^ 0x64086408u, sc.s, sc.t);
+    r[3] = hfma2_u32((h & 0x00F000F0u) ^ 0x64806480u, sc.s16, sc.t16);
   }
 }
 // Eight values of x in the order of the pairs.
@@ -69,11 +77,11 @@ __device__ __forceinline__ uint4 w4_x8(const uint2 &u) {   // e4m3
 }
 // The 32 of a 16-byte chunk.
 template <int CODE>
-__device__ __forceinline__ void w4_decode(const uint4 &q, uint32_t s2, uint32_t t2, uint32_t (&r)[16]) {
-  w4_decode8<CODE>(q.x, s2, t2, r);
-  w4_decode8<CODE>(q.y, s2, t2, r + 4);
-  w4_decode8<CODE>(q.z, s2, t2, r + 8);
-  w4_decode8<CODE>(q.w, s2, t2, r + 12);
+__device__ __forceinline__ void w4_decode(const uint4 &q, const W4Scale<CODE> &sc, uint32_t (&r)[16]) {
+  w4_decode8<CODE>(q.x, sc, r);
+  w4_decode8<CODE>(q.y, sc, r + 4);
+  w4_decode8<CODE>(q.z, sc, r + 8);
+  w4_decode8<CODE>(q.w, sc, r + 12);
 }
 
 // ---------------------------------------------------------------- x in f16
@@ -488,12 +496,9 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       const uint32_t ba = stage[s0], bb = stage[s1];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(bars->c_empty[st]));
-      uint32_t sa, sb, na, nb;
-      w4_scale<CODE>(ba, sa, na);
-      w4_scale<CODE>(bb, sb, nb);
       uint32_t f0[16], f1[16];
-      w4_decode<CODE>(v0, sa, na, f0);
-      w4_decode<CODE>(v1, sb, nb, f1);
+      w4_decode<CODE>(v0, W4Scale<CODE>(ba), f0);
+      w4_decode<CODE>(v1, W4Scale<CODE>(bb), f1);
       if (!mbar_wait_fast(bar(bars->a_empty[kq >> 1][ab]), aph, p.status)) break;
       tc_fence_after();
       tmem_st_32x32b_x16(ta + ab * 128, f0);
