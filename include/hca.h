@@ -496,7 +496,9 @@ int hca_add_rms_norm(const hca_norm_desc *d, const void *x, const void *res, con
  *   with ldn = N rounded up to 16; row_scale [groups*N] fp32.
  * x [T, groups*K] HCA_BF16 (x_scale NULL) or HCA_FP8E4M3 (x_scale [T] fp32);
  *   out [T, groups*N] HCA_F32 or HCA_BF16; row strides ldx, ldo elements
- *   (0 = dense).  Sums are fp32 and run in a fixed order.
+ *   (0 = dense).  Sums are fp32 and run in a fixed order.  A bf16 x enters them
+ *   exactly down to 2^-31 of the largest |x| of its token and group, and to
+ *   2^-39 of that largest below.
  * K a multiple of 32 and of scale_group (32, 64 or 128), K <= 32768; N >= 1,
  *   T >= 0 (T = 0 is a no-op), groups >= 1.  Rows of x must start at multiples
  *   of 16 bytes.  Meant for decode batches: beyond 64 tokens the weights are

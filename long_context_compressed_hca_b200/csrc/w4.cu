@@ -5,11 +5,14 @@
 //
 // A code (E2M1: 2 significant bits, INT4: 3) times an e4m3 scale (4 bits) is
 // exact in f16, so the weights enter the tensor cores as f16 without a
-// rounding.  x enters as f16 too: e4m3 values are f16 values; a bf16 row is
-// first multiplied by the power of two that puts its largest value into
-// [2^14, 2^15), which keeps every element to 2^-39 of that largest one, and
-// the sum is multiplied back.  The sums are fp32 (tensor memory).
+// rounding.  x enters as f16 too: e4m3 values are f16 values; a bf16 row (a
+// token's channels of one group) is multiplied by a power of two that leaves
+// its elements exact down to 2^-31 of its largest, and smaller ones to 2^-39
+// of that, and the sum is multiplied back.  The power of two comes from the
+// row or from those of its channels that a block has, never from another
+// group's.  The sums are fp32 (tensor memory).
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "lowbit.cuh"
@@ -231,7 +234,8 @@ struct W4Layout {
   static constexpr int ND = TN == 64 ? 1 : 2;
   static constexpr uint32_t kSecond = TN == 64 ? 64 : 32;   // column of the second accumulator in its pair
   static constexpr uint32_t x_off = NC * kStage;
-  static constexpr uint32_t xd_off = x_off + NX * kX, bar_off = xd_off + 512;
+  // factors of x; staged bf16: and maxima
+  static constexpr uint32_t xd_off = x_off + NX * kX, bar_off = xd_off + 2 * NX * TN * 4;
   static constexpr uint32_t bytes = bar_off + 512 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory");
 };
@@ -243,96 +247,111 @@ constexpr int kW4Threads = (kMma1 + 1) * 32;
 __device__ __forceinline__ void w4_dec_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kDecWarps * 32) : "memory"); }
 
 // The weight warps' staging of x: `units` units of TN tokens as f16 in the
-// layout that the MMAs read, and the factor per token.  A warp takes a token
-// of a unit at a time, a lane 8 channels.  bf16 values whose token has its
-// largest in [1, 2^15) (among the units staged here) are stored as they are:
-// f16 keeps them exactly down to 2^-17 and to 2^-25 below, half of the last
-// bit that the fp32 sum has of a term with the largest value.  A token outside
-// that range is stored again, scaled.
+// layout that the MMAs read, and the factor per group of the run and token,
+// xd[NX][TN].  A warp takes a token of a unit at a time, a lane 8 channels.
+// bf16 values are scaled as w4_x_kernel scales them, by the largest of the
+// token's values of the group that are staged here; they wait in registers for
+// it, a first batch of two is read again.
 template <int TN, int CODE, typename XT>
-__device__ __forceinline__ void w4_stage_x(const W4Params &p, const W4Work &wk, int u0, int units, uint8_t *xs, float *xd,
-                                           uint32_t *amax) {
-  constexpr int kBatch = 8;      // loads on their way before the first store
+__device__ __forceinline__ void w4_stage_x(const W4Params &p, const W4Work &wk, int u0, int units, uint8_t *xs, float *xd) {
+  constexpr int kBatch = 8;                // loads on their way before the first is used
+  constexpr int kPer = TN / kDecWarps, kUnits = kBatch / kPer;   // a warp's tokens of a unit, units of a batch
+  constexpr int kRows = W4Layout<TN>::NX * TN;
+  using V = std::conditional_t<sizeof(XT) == 1, uint2, uint4>;
   const int w = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31, tid = threadIdx.x - 64;
-  // unit un of the run: channels from k of group g (a run may pass into further tiles and groups)
-  int first = 0, g0 = 0, t0 = 0;
+  int first = 0, g0 = 0, t0 = 0;           // first unit's channels, group and tile of the group
   if (wk.x == kByUnit) {
     const int tile = u0 / wk.nk;
     first = u0 - tile * wk.nk;
     g0 = tile / wk.nb;
     t0 = tile - g0 * wk.nb;
   }
-  auto source = [&](int un, int row) -> const XT * {
-    int kb = first + un, g = g0, t = t0;
-    while (kb >= wk.nk) {
-      kb -= wk.nk;
-      if (++t == wk.nb) {
-        t = 0;
-        ++g;
-      }
+  V v[kBatch];
+  uint32_t sets;                           // group of the run of each unit of the batch, 4 bits each
+  auto load = [&](int b) {
+    int kb = first, t = t0, set = 0;
+    auto next = [&]() {
+      if (++kb < wk.nk) return;
+      kb = 0;
+      if (++t < wk.nb) return;
+      t = 0;
+      ++set;
+    };
+    for (int i = 0; i < b * kUnits; ++i) next();
+    sets = 0u;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (j > 0 && j % kPer == 0) next();
+      if (j % kPer == 0) sets |= (uint32_t)set << (4 * (j / kPer));
+      const int row = w + kDecWarps * (j % kPer), k = kb * kBlk + 8 * lane;
+      v[j] = V{};
+      if (b * kUnits + j / kPer < units && row < p.T && k < p.K)
+        v[j] = __ldg(reinterpret_cast<const V *>(static_cast<const XT *>(p.x) + row * p.ldx + (long long)(g0 + set) * p.K + k));
     }
-    const int k = kb * kBlk + 8 * lane;
-    return row < p.T && k < p.K ? static_cast<const XT *>(p.x) + (long long)row * p.ldx + (long long)g * p.K + k : nullptr;
+  };
+  // f(load j, unit, token, row of the factors) of a batch
+  auto each = [&](int b, auto f) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int un = b * kUnits + j / kPer, row = w + kDecWarps * (j % kPer);
+      if (un < units) f(v[j], un, row, (int)((sets >> (4 * (j / kPer))) & 15u) * TN + row);
+    }
   };
   auto store = [&](int un, int row, const uint4 &h) {
     *reinterpret_cast<uint4 *>(xs + un * W4Layout<TN>::kX + (lane / 8) * (TN * 128) + sw128_off(row, lane % 8)) = h;
   };
+  const int batches = (units + kUnits - 1) / kUnits;
   if constexpr (sizeof(XT) == 1) {
 #pragma unroll 1
-    for (int c = w; c < units * TN; c += kBatch * kDecWarps) {
-      uint2 u[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int cj = c + j * kDecWarps;
-        const XT *x = cj < units * TN ? source(cj / TN, cj % TN) : nullptr;
-        u[j] = x ? __ldg(reinterpret_cast<const uint2 *>(x)) : make_uint2(0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int cj = c + j * kDecWarps;
-        if (cj < units * TN) store(cj / TN, cj % TN, w4_x8<CODE>(u[j]));
-      }
+    for (int b = 0; b < batches; ++b) {
+      load(b);
+      each(b, [&](const V &u, int un, int row, int) { store(un, row, w4_x8<CODE>(u)); });
     }
-    if (tid < p.T) xd[tid] = p.x_scale[tid];
+    if (tid < kRows && tid % TN < p.T) xd[tid] = p.x_scale[tid % TN];
   } else {
-    if (tid < TN) amax[tid] = 0u;                  // |x| as bits, in the order of the values
-    w4_dec_sync();
-    auto f16 = [](const uint4 &u, float up) {
-      const float v[8] = {bf16_lo(u.x) * up, bf16_hi(u.x) * up, bf16_lo(u.y) * up, bf16_hi(u.y) * up,
-                          bf16_lo(u.z) * up, bf16_hi(u.z) * up, bf16_lo(u.w) * up, bf16_hi(u.w) * up};
-      return w4_x8<CODE>(v);
+    auto top = [](const V &u) {              // largest |x| of the warp's 256 as bits, in the order of the values
+      const uint32_t am = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+      return __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
     };
+    // 2^e <= the largest value < 2^(e + 1), e at least -110 so that 2^(14 - e) and its inverse are normal
+    auto expo = [](uint32_t am) { return max((int)(am >> 7) - 127, -110); };
+    auto f16 = [](const V &u, float up) {
+      const float f[8] = {bf16_lo(u.x) * up, bf16_hi(u.x) * up, bf16_lo(u.y) * up, bf16_hi(u.y) * up,
+                          bf16_lo(u.z) * up, bf16_hi(u.z) * up, bf16_lo(u.w) * up, bf16_hi(u.w) * up};
+      return w4_x8<CODE>(f);
+    };
+    if (units == 1) {
+      // a warp has its tokens' whole rows: no exchange (1 token x 512 x 4096: 8.1 us with it, 6.8 without)
+      load(0);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int row = w + kDecWarps * j, e = expo(top(v[j]));
+        store(0, row, f16(v[j], pow2f(14 - e)));
+        if (lane == 0) xd[row] = pow2f(e - 14);
+      }
+      return;
+    }
+    uint32_t *amax = reinterpret_cast<uint32_t *>(xd + kRows);
+    if (tid < kRows) amax[tid] = 0u;
+    load(0);
+    w4_dec_sync();
 #pragma unroll 1
-    for (int c = w; c < units * TN; c += kBatch * kDecWarps) {
-      uint4 u[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int cj = c + j * kDecWarps;
-        const XT *x = cj < units * TN ? source(cj / TN, cj % TN) : nullptr;
-        u[j] = x ? __ldg(reinterpret_cast<const uint4 *>(x)) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int cj = c + j * kDecWarps;
-        if (cj >= units * TN) break;
-        store(cj / TN, cj % TN, f16(u[j], 1.0f));
-        uint32_t am = __vmaxu2(__vmaxu2(u[j].x & 0x7FFF7FFFu, u[j].y & 0x7FFF7FFFu),
-                               __vmaxu2(u[j].z & 0x7FFF7FFFu, u[j].w & 0x7FFF7FFFu));
-        am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
-        if (lane == 0 && am) atomicMax(&amax[cj % TN], am);
-      }
+    for (int b = 0;;) {
+      each(b, [&](const V &u, int, int, int i) {
+        const uint32_t am = top(u);
+        if (lane == 0 && am) atomicMax(&amax[i], am);
+      });
+      if (++b == batches) break;
+      load(b);
     }
     w4_dec_sync();
-    // 2^e <= the largest value < 2^(e + 1), e at least -110 so that 2^(14 - e) and its inverse are normal
-    auto expo = [&](int row) { return max((int)(amax[row] >> 7) - 127, -110); };
-    auto kept = [&](int row) { return amax[row] == 0u || (expo(row) >= 0 && expo(row) < 15); };
 #pragma unroll 1
-    for (int c = w; c < units * TN; c += kDecWarps) {
-      if (kept(c % TN)) continue;
-      const XT *x = source(c / TN, c % TN);
-      store(c / TN, c % TN, f16(x ? *reinterpret_cast<const uint4 *>(x) : make_uint4(0, 0, 0, 0), pow2f(14 - expo(c % TN))));
+    for (int b = batches - 1;;) {
+      each(b, [&](const V &u, int un, int row, int i) { store(un, row, f16(u, pow2f(14 - expo(amax[i])))); });
+      if (--b < 0) break;
+      load(b);
     }
-    if (tid < p.T) xd[tid] = kept(tid) ? 1.0f : pow2f(expo(tid) - 14);
+    if (tid < kRows) xd[tid] = pow2f(expo(amax[tid]) - 14);
   }
 }
 
@@ -380,7 +399,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
-  float *xds = reinterpret_cast<float *>(smem + L::xd_off);   // staged x: factors [64], maxima [64]
+  float *xds = reinterpret_cast<float *>(smem + L::xd_off);   // [TN]; staged x: [NX][TN]
   const int u0 = wk.lo(blockIdx.x), u1 = wk.lo(blockIdx.x + 1), n = u1 - u0;
   pdl_trigger();
 
@@ -475,7 +494,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
     if (wk.x != kRing) {
       pdl_wait();   // x of the kernel before
       const int units = wk.x == kByUnit ? n : wk.nk;
-      w4_stage_x<TN, CODE, XT>(p, wk, u0, units, smem + L::x_off, xds, reinterpret_cast<uint32_t *>(xds + 64));
+      w4_stage_x<TN, CODE, XT>(p, wk, u0, units, smem + L::x_off, xds);
       fence_proxy_async();     // the tensor cores read it through the async proxy
       __syncwarp();
       if (lane == 0)
@@ -526,12 +545,14 @@ __global__ void __launch_bounds__(kW4Threads, 1)
     const uint32_t td = tmem + ((uint32_t)(q * 32) << 16);
     bool ok = wk.x == kRing || mbar_wait_fast(bar(bars->x_full[0]), 0, p.status);   // xds is written
     int piece = 0;
+    const int g0 = u0 / wk.nk / wk.ntt / wk.nb;
     for (int u = u0; u < u1 && ok; ++piece) {
       const int d = piece % L::ND;
       const int tile = u / wk.nk, end = min((tile + 1) * wk.nk, u1);
       const bool whole = u == tile * wk.nk && end == (tile + 1) * wk.nk;
       const int blk = tile / wk.ntt, g = blk / wk.nb, o = (blk - g * wk.nb) * kTileN + f;
       const int t0 = (tile - blk * wk.ntt) * TN, nt = min(TN, p.T - t0);
+      const float *xt = xds + (wk.x == kRing ? 0 : g - g0) * TN;
       if (wk.x == kRing) {
         if (f < nt) xds[f] = xd[g * p.T + t0 + f];
         asm volatile("bar.sync 2, 128;" ::: "memory");
@@ -549,7 +570,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
         tmem_ld_32x32b_x8(td + d * 64 + j0, v);
         tmem_ld_32x32b_x8(td + d * 64 + L::kSecond + j0, v1);
         float x[8], a[8];                   // read before the first store, which might be to the same memory for all
-        load8(xds + j0, x);                 // that the compiler knows
+        load8(xt + j0, x);                  // that the compiler knows
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = (__uint_as_float(v[j]) + __uint_as_float(v1[j])) * x[j] * rs;
