@@ -538,7 +538,8 @@ def kv_dequant_fp4(records, c, rd, out, slots=None, stream=None):
 
 class Fp4CacheHandle:
     """A cache of 4-bit records: rows [B, cap, rec], or with pages (int32
-    [B, max_pages]) rows [n_pages, cap, rec]; holds its tensors."""
+    [B, max_pages]; max_pages = 0: no entries) rows [n_pages, cap, rec]; holds
+    its tensors."""
 
     def __init__(self, rows, cap, pages=None):
         if rows.dim() != 3 or rows.shape[1] != cap:
@@ -546,7 +547,10 @@ class Fp4CacheHandle:
         if pages is not None and pages.dim() != 2:
             _bad("pages must be [B, max_pages]")
         self.rows, self.cap, self.pages = rows, cap, pages
-        self.struct = Fp4Cache(ptr(rows), cap, ptr(pages), 0 if pages is None else pages.shape[1], rows.shape[0])
+        # a page table without columns has no address, which by itself would mean a contiguous cache: one of no entries
+        none = pages is not None and pages.shape[1] == 0
+        self.struct = Fp4Cache(ptr(rows), 0 if none else cap, ptr(pages), 0 if pages is None else pages.shape[1],
+                               rows.shape[0])
 
 
 def fp4_cache(rows, cap, pages=None) -> Fp4CacheHandle:
