@@ -283,6 +283,9 @@ PyObject *attend_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const void *pg = take_or_null("pages", a[4], sp, kI32, dev);
     if (pr != cache->rows || pg != static_cast<const void *>(cache->pages))
       bad("the cache's tensors have moved since fp4_cache made it");
+    if (cache->cap > 0 && nrec != (int64_t)cache->n_pages * cache->cap)
+      bad("the cache has " + std::to_string(nrec) + " records, " + std::to_string((int64_t)cache->n_pages * cache->cap) +
+          " when fp4_cache made it");
     if (a[4] == Py_None && rows.size(0) != B)
       bad("the cache has " + std::to_string(rows.size(0)) + " sequences, expected " + std::to_string(B));
     const void *pi = take_or_null("idx", a[5], si, kI32, dev);
