@@ -87,6 +87,15 @@ const void *take(const char *name, PyObject *o, c10::IntArrayRef shape, Types ty
 const void *take_or_null(const char *name, PyObject *o, c10::IntArrayRef shape, Types ty, int dev, int64_t ld = 0) {
   return o == Py_None ? nullptr : take(name, o, shape, ty, dev, ld);
 }
+// Address of a tensor that the call writes: a lazy clone gets memory of its own
+// first.  Asked for before the inputs', one of which may be the same tensor.
+void *take_out(const char *name, const at::Tensor &t, c10::IntArrayRef shape, Types ty, int dev, int64_t ld = 0) {
+  take(name, t, shape, ty, dev, ld);
+  return t.mutable_data_ptr();
+}
+void *take_out(const char *name, PyObject *o, c10::IntArrayRef shape, Types ty, int dev, int64_t ld = 0) {
+  return take_out(name, tensor(name, o), shape, ty, dev, ld);
+}
 struct Scratch {
   void *p = nullptr;
   size_t n = 0;
@@ -95,7 +104,7 @@ Scratch scratch(PyObject *o, int dev) {
   Scratch s;
   if (o == Py_None) return s;
   const at::Tensor &t = tensor("ws", o);
-  s.p = const_cast<void *>(take("ws", t, t.sizes(), Types{t.scalar_type(), t.scalar_type(), 1}, dev));
+  s.p = take_out("ws", t, t.sizes(), Types{t.scalar_type(), t.scalar_type(), 1}, dev);
   s.n = t.numel() * t.element_size();
   return s;
 }
@@ -176,21 +185,20 @@ PyObject *add_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int dev = device_of(x);
     const int64_t shape[2] = {d->rows, d->d}, row[1] = {d->d};
     const Types rt = types_of(d->res_dtype);
+    void *pro = a[4] == Py_None ? nullptr : take_out("res_out", a[4], shape, rt, dev, d->ldr);
     const void *px = take("x", x, shape, types_of(d->x_dtype), dev, d->ldx);
     const void *pr = take_or_null("res", a[2], shape, rt, dev, d->ldr);
     const void *pg = take_or_null("gamma", a[3], row, kF32, dev);
-    const void *pro = take_or_null("res_out", a[4], shape, rt, dev, d->ldr);
-    const void *po = take("out", a[5], shape, types_of(d->out_dtype), dev, d->ldo);
-    const void *ps = nullptr;
+    void *po = take_out("out", a[5], shape, types_of(d->out_dtype), dev, d->ldo);
+    void *ps = nullptr;
     if (d->out_dtype == HCA_FP8E4M3) {
       if (a[6] == Py_None) bad("an e4m3 output needs out_scale");
       const int64_t ss[2] = {d->rows, d->scale_group > 0 ? d->d / d->scale_group : 1};
-      ps = take("out_scale", a[6], ss, kF32, dev);
+      ps = take_out("out_scale", a[6], ss, kF32, dev);
     }
     void *s = stream_of(a[7]);
     return unlocked([&] {
-      return hca_add_rms_norm(d.get(), px, pr, static_cast<const float *>(pg), const_cast<void *>(pro),
-                              const_cast<void *>(po), static_cast<float *>(const_cast<void *>(ps)), s);
+      return hca_add_rms_norm(d.get(), px, pr, static_cast<const float *>(pg), pro, po, static_cast<float *>(ps), s);
     });
   });
 }
@@ -213,25 +221,24 @@ PyObject *w4_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const void *pc = take("codes", a[3], sc, kU8, dev);
     const void *pw = take("scales", a[4], ss, kE4M3, dev);
     const void *pr = take("row_scale", a[5], sr, kF32, dev);
-    const void *po = take("out", a[6], so, types_of(d->out_dtype), dev, d->ldo);
+    void *po = take_out("out", a[6], so, types_of(d->out_dtype), dev, d->ldo);
     const Scratch ws = scratch(a[7], dev);
     void *s = stream_of(a[8]);
     return unlocked([&] {
-      return hca_w4_linear(d.get(), px, static_cast<const float *>(ps), pc, pw, static_cast<const float *>(pr),
-                           const_cast<void *>(po), ws.p, ws.n, s);
+      return hca_w4_linear(d.get(), px, static_cast<const float *>(ps), pc, pw, static_cast<const float *>(pr), po, ws.p,
+                           ws.n, s);
     });
   });
 }
 
-// Address and number of the records in t [.., record bytes].
-const void *records(const char *name, const at::Tensor &t, int c, int rd, int dev, int64_t *n) {
+// Number of the records in t [.., record bytes].
+int64_t records(const char *name, const at::Tensor &t, int c, int rd) {
   const int64_t rec = (int64_t)hca_kv_fp4_row_bytes(c, rd);
   if (rec == 0) bad("unsupported (c, rd) = (" + std::to_string(c) + ", " + std::to_string(rd) + ")");
   if (t.dim() == 0 || t.size(-1) != rec) {
     bad(std::string(name) + " has shape " + shape_name(t.sizes()) + ", expected records of " + std::to_string(rec) + " bytes");
   }
-  *n = t.numel() / rec;
-  return take(name, t, t.sizes(), kU8, dev);
+  return t.numel() / rec;
 }
 
 // (x, c, rd, records, slots, stream)
@@ -239,14 +246,14 @@ PyObject *kv_quant_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return call(n, 6, [&] {
     const at::Tensor &x = tensor("x", a[0]), &r = tensor("records", a[3]);
     const int c = int32("c", a[1]), rd = int32("rd", a[2]), dev = device_of(x);
-    int64_t nrec;
-    const void *po = records("records", r, c, rd, dev, &nrec);
+    const int64_t nrec = records("records", r, c, rd);
+    void *po = take_out("records", r, r.sizes(), kU8, dev);
     const int64_t rows = x.dim() ? x.size(0) : 0, sx[2] = {rows, c}, sr[1] = {rows};
     const void *px = take("x", x, sx, kF32orBF16, dev);
     const void *ps = take_or_null("slots", a[4], sr, kI64, dev);
     void *s = stream_of(a[5]);
     return unlocked([&] {
-      return hca_kv_quant_fp4(px, code_of(x), rows, c, rd, const_cast<void *>(po), nrec, static_cast<const long long *>(ps), s);
+      return hca_kv_quant_fp4(px, code_of(x), rows, c, rd, po, nrec, static_cast<const long long *>(ps), s);
     });
   });
 }
@@ -256,14 +263,14 @@ PyObject *kv_dequant_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return call(n, 6, [&] {
     const at::Tensor &r = tensor("records", a[0]), &out = tensor("out", a[3]);
     const int c = int32("c", a[1]), rd = int32("rd", a[2]), dev = device_of(out);
-    int64_t nrec;
-    const void *pi = records("records", r, c, rd, dev, &nrec);
+    const int64_t nrec = records("records", r, c, rd);
+    const void *pi = take("records", r, r.sizes(), kU8, dev);
     const int64_t rows = out.dim() ? out.size(0) : 0, so[2] = {rows, c}, sr[1] = {rows};
-    const void *po = take("out", out, so, kBF16, dev);
+    void *po = take_out("out", out, so, kBF16, dev);
     const void *ps = take_or_null("slots", a[4], sr, kI64, dev);
     void *s = stream_of(a[5]);
     return unlocked([&] {
-      return hca_kv_dequant_fp4(pi, nrec, static_cast<const long long *>(ps), rows, c, rd, const_cast<void *>(po), s);
+      return hca_kv_dequant_fp4(pi, nrec, static_cast<const long long *>(ps), rows, c, rd, po, s);
     });
   });
 }
@@ -277,9 +284,10 @@ PyObject *attend_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int dev = device_of(q);
     const int64_t B = d->B, c = d->c, sq[3] = {B, d->n_h, c}, si[2] = {B, d->k}, sw[3] = {B, d->w > 0 ? d->w : 1, c},
                   sh[1] = {d->n_h}, sb[1] = {B}, sp[2] = {B, cache->max_pages};
-    const void *pq = take("q", q, sq, kBF16, dev), *po = take("o", a[10], sq, kBF16, dev);
-    int64_t nrec;
-    const void *pr = records("cache rows", rows, d->c, d->rd, dev, &nrec);
+    const void *pq = take("q", q, sq, kBF16, dev);
+    void *po = take_out("o", a[10], sq, kBF16, dev);
+    const int64_t nrec = records("cache rows", rows, d->c, d->rd);
+    const void *pr = take("cache rows", rows, rows.sizes(), kU8, dev);
     const void *pg = take_or_null("pages", a[4], sp, kI32, dev);
     if (pr != cache->rows || pg != static_cast<const void *>(cache->pages))
       bad("the cache's tensors have moved since fp4_cache made it");
@@ -297,7 +305,7 @@ PyObject *attend_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *s = stream_of(a[12]);
     return unlocked([&] {
       return hca_attend_fp4(d.get(), pq, cache.get(), static_cast<const int32_t *>(pi), pk, static_cast<const float *>(ps),
-                            static_cast<const int32_t *>(pp), max_pos, const_cast<void *>(po), ws.p, ws.n, s);
+                            static_cast<const int32_t *>(pp), max_pos, po, ws.p, ws.n, s);
     });
   });
 }
