@@ -507,15 +507,17 @@ def w4_linear(d: W4Desc, x, x_scale, codes, scales, row_scale, out, ws, stream=N
 
 
 def w4_quantize(d: W4Desc, w, stream=None):
-    """(codes, scales, row_scale) of weights w [groups*N, K], as w4_linear takes them."""
+    """(codes, scales, row_scale) of weights w [groups*N, K], as w4_linear takes them.  They are allocated on the
+    stream that the call runs on: another one that uses them waits for it."""
     if not w.is_cuda or w.get_device() != torch.cuda.current_device():
         _bad(f"w must be on the current CUDA device (it is on {w.device})")
     if w.dtype not in (torch.float32, torch.bfloat16) or w.shape != (d.groups * d.N, d.K) or not w.is_contiguous():
         _bad(f"w must be contiguous float32 or bfloat16 of shape {(d.groups * d.N, d.K)}, got {w.dtype} {tuple(w.shape)}")
-    codes = torch.empty(d.groups * d.N, d.K // 2, dtype=torch.uint8, device=w.device)
-    scales = torch.empty(d.groups, d.K // max(d.scale_group, 1), (d.N + 15) // 16 * 16, dtype=torch.uint8,
-                         device=w.device)
-    row_scale = torch.empty(d.groups * d.N, dtype=torch.float32, device=w.device)
+    with torch.cuda.stream(stream):       # what the current stream's allocator gives may still be in use there
+        codes = torch.empty(d.groups * d.N, d.K // 2, dtype=torch.uint8, device=w.device)
+        scales = torch.empty(d.groups, d.K // max(d.scale_group, 1), (d.N + 15) // 16 * 16, dtype=torch.uint8,
+                             device=w.device)
+        row_scale = torch.empty(d.groups * d.N, dtype=torch.float32, device=w.device)
     check(lib().hca_w4_quantize(d, ptr(w), DTYPE_CODE[w.dtype], ptr(codes), ptr(scales), ptr(row_scale),
                                 stream_handle(stream)))
     return codes, scales, row_scale
