@@ -112,8 +112,8 @@ struct Fp4Layout {
 };
 
 struct Fp4Bars {
-  uint64_t q_full, q_empty, o_empty, all_done, kv_full[8], kv_empty[8], s_full[SP], s_empty[SP], p_full[SP], pv_done[SP];
-  uint32_t tmem;
+  uint64_t q_full, q_empty, o_empty, all_done, settled, kv_full[8], kv_empty[8], s_full[SP], s_empty[SP], p_full[SP], pv_done[SP];
+  uint32_t tmem, ran_out;
 };
 
 // This CTA's run of tiles: from tile `j0` of sequence `b0`, `n` tiles; `before`
@@ -192,6 +192,7 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
   const unsigned char *rp0 = none, *rp1 = none;
   int pg = 0, st = 0;
   uint32_t ph = 1;
+  const Waits wait{p.status, &bars->ran_out};
   while (true) {
     // ---- codes' address of t1 from the page that the round before asked for
     rp1 = none;
@@ -234,7 +235,7 @@ __device__ __forceinline__ void fp4_load(const AttendFp4Params &p, const Fp4Plan
     const uint32_t full = smem_u32(&bars->kv_full[st]);
     uint32_t ex = 0u;
     if (t0.kind) {
-      if (!mbar_wait_fast(smem_u32(&bars->kv_empty[st]), ph, p.status)) break;
+      wait(smem_u32(&bars->kv_empty[st]), ph);
       uint32_t *mask = reinterpret_cast<uint32_t *>(smem + L::mask_off) + 2 * st;
       const uint32_t tdst = sbase + st * L::NKB * kTileBytes;
       if (t0.kind == 2) {
@@ -327,12 +328,11 @@ __device__ __forceinline__ void fp4_mma(const AttendFp4Params &p, const Fp4Plan 
   int ks = 0, vs = 0;                     // stage of the next S and of the next P V
   uint32_t kph = 0, gs = 0, gv = 0;       // tiles issued so far
   int npiece = 0;
-  bool ok = true;
+  const Waits wait{p.status, &bars->ran_out};
   auto issue_pv = [&](bool first) {
     const int st = gv % SP;
-    ok = mbar_wait_fast(bar(bars->p_full[st]), (gv / SP) & 1, p.status) &&
-         (!first || mbar_wait_fast(bar(bars->o_empty), (npiece & 1) ^ 1, p.status));
-    if (!ok) return;
+    wait(bar(bars->p_full[st]), (gv / SP) & 1);
+    if (first) wait(bar(bars->o_empty), (npiece & 1) ^ 1);
     tc_fence_after();
     if (elect_one()) {
       const uint64_t pd = sdesc_sw128(sbase + L::p_off + st * kTileBytes, 16, 1024);
@@ -350,13 +350,12 @@ __device__ __forceinline__ void fp4_mma(const AttendFp4Params &p, const Fp4Plan 
     if (++vs == L::NS) vs = 0;
     ++gv;
   };
-  for (Fp4Walk w = fp4_walk(run); ok && fp4_next(p, pl, run, w); ++npiece) {
-    ok = mbar_wait_fast(bar(bars->q_full), npiece & 1, p.status);
-    for (int j = 0; j < w.cnt && ok; ++j) {
+  for (Fp4Walk w = fp4_walk(run); fp4_next(p, pl, run, w); ++npiece) {
+    wait(bar(bars->q_full), npiece & 1);
+    for (int j = 0; j < w.cnt; ++j) {
       const int st = gs % SP;
-      ok = mbar_wait_fast(bar(bars->kv_full[ks]), kph, p.status) &&
-           mbar_wait_fast(bar(bars->s_empty[st]), ((gs / SP) & 1) ^ 1, p.status);
-      if (!ok) break;
+      wait(bar(bars->kv_full[ks]), kph);
+      wait(bar(bars->s_empty[st]), ((gs / SP) & 1) ^ 1);
       fence_proxy_async();                // window rows come by cp.async
       tc_fence_after();
       if (elect_one()) {
@@ -376,9 +375,10 @@ __device__ __forceinline__ void fp4_mma(const AttendFp4Params &p, const Fp4Plan 
       ++gs;
       if (j > 0) issue_pv(j == 1);
     }
-    if (ok) issue_pv(w.cnt == 1);
+    issue_pv(w.cnt == 1);
   }
-  if (ok && pl.S && run.n > 0 && elect_one()) umma_commit(bar(bars->all_done));   // the loaders wait for it
+  if (pl.S && run.n > 0 && elect_one()) umma_commit(bar(bars->all_done));   // the loaders wait for it
+  wait.settle(bar(bars->settled));
   __syncwarp();
 }
 
@@ -429,6 +429,7 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
   int ks = 0, npiece = 0;
   uint32_t kph = 0;
   int before = run.before;
+  const Waits wait{p.status, &bars->ran_out};
 
   // Q into tensor memory, 64 channels of either half at a time: read 8 lanes to
   // 128 contiguous bytes and turned through this warp's 4 KB of the P buffers
@@ -489,13 +490,13 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
       const int st = g % SP;
       const uint32_t ph = (g / SP) & 1;
       // the loaders' mask of this stage
-      if (!mbar_wait_fast(bar(bars->kv_full[ks]), kph, p.status)) return;
+      wait(bar(bars->kv_full[ks]), kph);
       const uint32_t vmask = reinterpret_cast<const uint32_t *>(smem + L::mask_off)[2 * ks + half];
       if (++ks == L::NS) {
         ks = 0;
         kph ^= 1;
       }
-      if (!mbar_wait_fast(bar(bars->s_full[st]), ph, p.status)) return;
+      wait(bar(bars->s_full[st]), ph);
       tc_fence_after();
       uint32_t sv[32];
       tmem_ld_16x32bx2_x16<32>(tmem + lane_S + st * KT, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
@@ -524,7 +525,7 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
       }
       if (__any_sync(0xffffffffu, need)) {
         // rescale O once the previous tile's P V has landed
-        if (!mbar_wait_fast(bar(bars->pv_done[(g - 1) % SP]), ((g - 1) / SP) & 1, p.status)) return;
+        wait(bar(bars->pv_done[(g - 1) % SP]), ((g - 1) / SP) & 1);
         tc_fence_after();
 #pragma unroll 1
         for (int c0 = 0; c0 < C / 2; c0 += 16) {
@@ -548,7 +549,7 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
       }
       l += ps[0] + ps[1];
       // P buffer st is free once the P V of two tiles ago has completed
-      if (!mbar_wait_fast(bar(bars->pv_done[st]), ph ^ 1, p.status)) return;
+      wait(bar(bars->pv_done[st]), ph ^ 1);
       uint8_t *prow = smem + L::p_off + st * kTileBytes;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -561,14 +562,11 @@ __device__ __forceinline__ void fp4_softmax(const AttendFp4Params &p, const Fp4P
     }
 
     // the last P V, then the next piece's Q before this one's epilogue, so that its first S need not wait for that
-    {
-      const uint32_t gl = g - 1;
-      if (!mbar_wait_fast(bar(bars->pv_done[gl % SP]), (gl / SP) & 1, p.status)) return;
-    }
+    wait(bar(bars->pv_done[(g - 1) % SP]), ((g - 1) / SP) & 1);
     Fp4Walk wn = w;
     more = fp4_next(p, pl, run, wn);
     if (more) {
-      if (!mbar_wait_fast(bar(bars->q_empty), npiece & 1, p.status)) return;
+      wait(bar(bars->q_empty), npiece & 1);
       asm volatile("bar.sync 1, 128;" ::: "memory");   // all warps are past the P V that reads all of P
       write_q(wn.b);
     }
@@ -732,6 +730,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
     mbar_init(bar(bars->q_empty), 1);
     mbar_init(bar(bars->o_empty), 4);
     mbar_init(bar(bars->all_done), 1);
+    mbar_init(bar(bars->settled), 1);
+    bars->ran_out = 0u;
     for (int i = 0; i < L::NS; ++i) {
       mbar_init(bar(bars->kv_full[i]), kLoadWarps * 33);   // every thread's copies, every warp's stores
       mbar_init(bar(bars->kv_empty[i]), 1);
@@ -846,7 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_fp4_kernel(AttendFp4Params
   if (warp >= kLoad0) {
     fp4_load<C>(p, pl, run, smem, bars);
     // a cluster's CTA has one piece; its sums are there once all MMAs have run (pv_done's phases are not followed here)
-    if (pl.S && run.n > 0 && mbar_wait_fast(bar(bars->all_done), 0, p.status)) {
+    if (pl.S && run.n > 0) {
+      Waits{p.status, &bars->ran_out}(bar(bars->all_done), 0);
       tc_fence_after();
       __syncwarp();
       fp4_part_store<C>(p, reinterpret_cast<float4 *>(smem), 0, tmem, warp & 3, 1 + (warp - kLoad0) / 4, 3);

@@ -87,23 +87,41 @@ __device__ __forceinline__ uint32_t e2m1_code(float v) {
   return k ? (uint32_t)k | (v < 0.f ? 8u : 0u) : 0u;
 }
 
-// Bounded wait as mbar_wait, limited by the SM's cycle counter: reading the
+// Bounded waits of a thread, limited by the SM's cycle counter: reading the
 // global timer on every wait that does not pass at once costs more than the
-// wait in a pipeline of a few hundred cycles per step.
+// wait in a pipeline of a few hundred cycles per step.  After one that ran out
+// the thread waits no more and goes on with whatever is there (every access
+// stays in its buffers whatever the data), the status being set: leaving a loop
+// instead would part the lanes of a warp, and leave other warps at a named
+// barrier for good.  Only a lane on its own may leave.
 constexpr long long kWaitLimitCycles = 4000000000ll;   // about 2 s
-__device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, int *status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (;;) {
+struct Waits {
+  int *status;
+  uint32_t *any;                // shared memory, 0 at first: whether a wait of the block ran out
+  mutable bool out = false;     // one of this thread's did
+  __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity) || out) return;
+    out = !until(bar, parity);
+  }
+  // false if the phase has not passed
+  __device__ __forceinline__ bool until(uint32_t bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (clock64() - t0 > kWaitLimitCycles) {
-      set_timeout_status(status);
-      return false;
+      for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        set_timeout_status(status);
+        *static_cast<volatile uint32_t *>(any) = 1u;
+        return false;
+      }
     }
   }
-}
+  // A warp that issues MMAs, when it has issued its last: after a wait that ran
+  // out those under way end before tensor memory is given back.
+  __device__ __forceinline__ void settle(uint32_t bar) const;
+};
 
 // The codes of eight values, v[i] in nibble i: the conversion instruction's
 // nearest, ties to even, saturating; zero as +0.
@@ -127,6 +145,12 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
+}
+
+__device__ __forceinline__ void Waits::settle(uint32_t bar) const {
+  if (!__any_sync(0xffffffffu, *static_cast<volatile uint32_t *>(any))) return;
+  if (elect_one()) umma_commit(bar);
+  until(bar, 0);
 }
 
 // 2^k, -126 <= k <= 127.

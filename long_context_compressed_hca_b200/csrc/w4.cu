@@ -365,13 +365,14 @@ __global__ void __launch_bounds__(kW4Threads, 1)
   const uint32_t sbase = smem_u32(smem);
   struct Bars {
     uint64_t c_full[L::NC], c_empty[L::NC], x_full[L::NX], x_empty[L::NX], a_full[2][kNA], a_empty[2][kNA], d_full[2],
-        d_empty[2];
-    uint32_t tmem;
+        d_empty[2], done[2];
+    uint32_t tmem, ran_out;
   };
   static_assert(sizeof(Bars) <= 512, "barriers");
   Bars *bars = reinterpret_cast<Bars *>(smem + L::bar_off);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   auto bar = [&](uint64_t &b) { return smem_u32(&b); };
+  const Waits wait{p.status, &bars->ran_out};
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::NC; ++i) {
       mbar_init(bar(bars->c_full[i]), 1);
@@ -388,7 +389,9 @@ __global__ void __launch_bounds__(kW4Threads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(bars->d_full[i]), 2);
       mbar_init(bar(bars->d_empty[i]), 4);
+      mbar_init(bar(bars->done[i]), 1);
     }
+    bars->ran_out = 0u;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
         const int sshift = p.G == 32 ? 3 : p.G == 64 ? 2 : 1;   // scale rows of a unit: 2^sshift
         for (int i = 0; i < n; ++i, next()) {
           const int st = i % L::NC;
-          if (!mbar_wait_fast(bar(bars->c_empty[st]), ((i / L::NC) & 1) ^ 1, p.status)) break;
+          if (!wait.until(bar(bars->c_empty[st]), ((i / L::NC) & 1) ^ 1)) break;
           const uint32_t b = bar(bars->c_full[st]), a = sbase + st * L::kStage;
           mbar_arrive_expect_tx(b, bytes);
           tma_load_3d(a, &tmC, kb * (kBlk / 2), n0, g, b);
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
         pdl_wait();
         for (int i = 0; i < n; ++i, next()) {
           const int st = i % L::NX;
-          if (!mbar_wait_fast(bar(bars->x_empty[st]), ((i / L::NX) & 1) ^ 1, p.status)) break;
+          if (!wait.until(bar(bars->x_empty[st]), ((i / L::NX) & 1) ^ 1)) break;
           const uint32_t b = bar(bars->x_full[st]), a = sbase + L::x_off + st * L::kX;
           mbar_arrive_expect_tx(b, L::kX);
 #pragma unroll
@@ -456,16 +459,14 @@ __global__ void __launch_bounds__(kW4Threads, 1)
     int ab = 0, xs = 0, left = wk.nk - u0 % wk.nk;   // left: units of the tile
     if (wk.x == kByBlock) xs = wk.nk - left;
     uint32_t aph = 0, xph = 0;
-    bool ok = true;
-    for (int i = 0, piece = 0; i < n && ok; ++piece) {
+    for (int i = 0, piece = 0; i < n; ++piece) {
       const int end = min(n, i + left), d = piece % L::ND;   // units [i, end) of one tile
       left = wk.nk;
-      ok = mbar_wait_fast(bar(bars->d_empty[d]), ((piece / L::ND) & 1) ^ 1, p.status);
+      wait(bar(bars->d_empty[d]), ((piece / L::ND) & 1) ^ 1);
       const uint32_t td = tmem + d * 64 + half * L::kSecond;
-      for (uint32_t acc = 0; i < end && ok; ++i, acc = 1) {
-        ok = mbar_wait_fast(bar(bars->x_full[xs]), xph, p.status) &&
-             mbar_wait_fast(bar(bars->a_full[half][ab]), aph, p.status);
-        if (!ok) break;
+      for (uint32_t acc = 0; i < end; ++i, acc = 1) {
+        wait(bar(bars->x_full[xs]), xph);
+        wait(bar(bars->a_full[half][ab]), aph);
         tc_fence_after();
         if (elect_one()) {
           const uint64_t xdesc = xdesc0 + xs * (L::kX >> 4);
@@ -490,6 +491,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
         }
       }
     }
+    wait.settle(bar(bars->done[half]));
   } else if (warp < kEpi0) {
     if (wk.x != kRing) {
       pdl_wait();   // x of the kernel before
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
     int st = 0, ab = 0;
     uint32_t cph = 0, aph = 1;
     for (int i = 0; i < n; ++i) {
-      if (!mbar_wait_fast(bar(bars->c_full[st]), cph, p.status)) break;
+      wait(bar(bars->c_full[st]), cph);
       const uint8_t *stage = smem + st * L::kStage;
       const uint4 v0 = *reinterpret_cast<const uint4 *>(stage + o0), v1 = *reinterpret_cast<const uint4 *>(stage + o1);
       const uint32_t ba = stage[s0], bb = stage[s1];
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       uint32_t f0[16], f1[16];
       w4_decode<CODE>(v0, W4Scale<CODE>(ba), f0);
       w4_decode<CODE>(v1, W4Scale<CODE>(bb), f1);
-      if (!mbar_wait_fast(bar(bars->a_empty[kq >> 1][ab]), aph, p.status)) break;
+      wait(bar(bars->a_empty[kq >> 1][ab]), aph);
       tc_fence_after();
       tmem_st_32x32b_x16(ta + ab * 128, f0);
       tmem_st_32x32b_x16(ta + ab * 128 + 16, f1);
@@ -543,10 +545,10 @@ __global__ void __launch_bounds__(kW4Threads, 1)
     pdl_wait();   // xd of the kernel before; out may still be read by it
     const int q = warp & 3, f = q * 32 + lane;
     const uint32_t td = tmem + ((uint32_t)(q * 32) << 16);
-    bool ok = wk.x == kRing || mbar_wait_fast(bar(bars->x_full[0]), 0, p.status);   // xds is written
+    if (wk.x != kRing) wait(bar(bars->x_full[0]), 0);   // xds is written
     int piece = 0;
     const int g0 = u0 / wk.nk / wk.ntt / wk.nb;
-    for (int u = u0; u < u1 && ok; ++piece) {
+    for (int u = u0; u < u1; ++piece) {
       const int d = piece % L::ND;
       const int tile = u / wk.nk, end = min((tile + 1) * wk.nk, u1);
       const bool whole = u == tile * wk.nk && end == (tile + 1) * wk.nk;
@@ -561,8 +563,7 @@ __global__ void __launch_bounds__(kW4Threads, 1)
       if (whole && o < p.N) rs = p.row_scale[(long long)g * p.N + o] * (CODE == HCA_W4_INT4 ? 512.f : 1.f);
       float *pp = part + (long long)wk.slot(blockIdx.x, tile) * min(TN, p.T) * kTileN + f;
       OT *po = static_cast<OT *>(p.out) + (long long)t0 * p.ldo + (long long)g * p.N + o;
-      ok = mbar_wait_fast(bar(bars->d_full[d]), (piece / L::ND) & 1, p.status);
-      if (!ok) break;
+      wait(bar(bars->d_full[d]), (piece / L::ND) & 1);
       tc_fence_after();
 #pragma unroll 1
       for (int j0 = 0; j0 < nt; j0 += 8) {
