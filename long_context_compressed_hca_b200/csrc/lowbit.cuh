@@ -12,9 +12,10 @@
 
 namespace hca {
 
-// Blocks of `threads` threads that all SMs hold at once by their registers
-// (kernels without much shared memory): the grid of a kernel whose blocks
-// stride over its work, so that no partly filled wave follows the first.
+// Blocks of `threads` threads that all SMs hold at once by their registers and
+// by the 32 blocks of an SM (kernels without much shared memory): the grid of a
+// kernel whose blocks stride over its work, so that no partly filled wave
+// follows the first.
 template <auto Kernel>
 int resident_blocks(int threads) {
   static std::atomic<int> regs_dev[kMaxDevices];
@@ -27,7 +28,7 @@ int resident_blocks(int threads) {
     }
     regs = (std::max(a.numRegs, 1) + 7) / 8 * 8;
   }
-  return num_sms() * std::max(1, std::min(2048, 65536 / regs) / threads);
+  return num_sms() * std::max(1, std::min({2048 / threads, 65536 / regs / threads, 32}));
 }
 
 // Two f16 values (low half: low nibble) of one byte of E2M1 codes, by the
