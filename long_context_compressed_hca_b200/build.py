@@ -5,12 +5,14 @@ Each .cu under csrc/ is compiled by nvcc for sm_100a to an object in parallel,
 then linked into long_context_compressed_hca_b200/libhca.so with the CUDA
 runtime linked statically.  csrc/host/torch_call.cpp, the path from tensors to
 some of its calls, becomes the extension module _torch_call.so, linked to
-libhca.so and torch.  Objects are rebuilt when their source or any header is
-newer.
+libhca.so and torch; libhca.so itself needs neither torch nor the extension, and
+is linked before an error of the extension is raised.  Without torch there is no
+extension.  Objects are rebuilt when their source or any header is newer.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -68,7 +70,6 @@ def _compile_call(obj: str, verbose: bool):
           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
           "-isystem", sysconfig.get_paths()["include"],
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"], "g++ torch_call.cpp", verbose)
-    return ""
 
 
 def _link_call(obj: str, verbose: bool):
@@ -93,12 +94,14 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             jobs.append((s, o))
     call_obj = os.path.join(BUILD, "torch_call.o")
     call_mtime = max(os.path.getmtime(CALL_SRC), os.path.getmtime(os.path.join(ROOT, "include", "hca.h")))
-    call_job = force or not os.path.exists(call_obj) or os.path.getmtime(call_obj) < call_mtime
+    has_torch = importlib.util.find_spec("torch") is not None
+    call_job = has_torch and (force or not os.path.exists(call_obj) or os.path.getmtime(call_obj) < call_mtime)
+    call = None
     if jobs or call_job:
         with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
             futs = {ex.submit(_compile, s, o, extra, verbose): s for s, o in jobs}
             if call_job:
-                futs[ex.submit(_compile_call, call_obj, verbose)] = CALL_SRC
+                call = ex.submit(_compile_call, call_obj, verbose)
             for f in cf.as_completed(futs):
                 warn = f.result()
                 if verbose and warn.strip():
@@ -108,7 +111,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         _run([nvcc(), "-shared", "-o", LIB + ".tmp"] + objs + ARCH +
              ["-cudart", "static", "-Xcompiler", "-fPIC", "-Xlinker", "-soname=libhca.so"], "link", verbose)
         os.replace(LIB + ".tmp", LIB)
-    if call_job or not os.path.exists(CALL) or os.path.getmtime(CALL) < os.path.getmtime(call_obj):
+    if call:
+        call.result()
+    if has_torch and (call_job or not os.path.exists(CALL) or os.path.getmtime(CALL) < os.path.getmtime(call_obj)):
         _link_call(call_obj, verbose)
     return LIB
 
