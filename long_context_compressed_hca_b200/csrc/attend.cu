@@ -192,6 +192,8 @@ __global__ void __launch_bounds__(128) attend_combine(AttendParams p) {
     rcs[32 + i] = sn;
   }
   __syncthreads();
+  // splits without key tiles are the last ones; their parts were never written
+  const int all = (ks.nk + 63) / 64, per = (all + p.nsplit - 1) / p.nsplit, live = per ? (all + per - 1) / per : 0;
   const int per_head = C / 4;
   for (int e = threadIdx.x; e < 4 * per_head; e += blockDim.x) {
     const int hh = e / per_head, r = hg * 4 + hh;
@@ -200,9 +202,8 @@ __global__ void __launch_bounds__(128) attend_combine(AttendParams p) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const float *base = p.part_o + ((long long)bq * p.nsplit * 64 + r) * C + col;
 #pragma unroll 4
-    for (int sp = 0; sp < p.nsplit; ++sp) {
+    for (int sp = 0; sp < live; ++sp) {
       const float w = wsc[hh][sp];
-      if (w == 0.f) continue;   // an empty split's part was never written
       const float4 v = *reinterpret_cast<const float4 *>(base + (long long)sp * 64 * C);
       acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
     }
