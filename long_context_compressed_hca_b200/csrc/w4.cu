@@ -192,7 +192,7 @@ W4Work w4_work(const W4Params &p, int tn) {
   w.rem = w.U / w.gran - w.base * w.G;
   const int run = (w.base + (w.rem > 0)) * w.gran;   // the longest
   const bool block = p.groups == 1 && w.nk <= NX;
-  w.x = w.ntt > 1 ? kRing : block && w.nk <= run ? kByBlock : run <= NX ? kByUnit : block ? kByBlock : kRing;
+  w.x = w.ntt > 1 ? kRing : block && w.nk <= run ? kByBlock : run <= NX ? kByUnit : kRing;
   return w;
 }
 constexpr int kMaxT = 4096;               // tokens of one launch
