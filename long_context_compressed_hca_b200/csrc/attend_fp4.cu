@@ -947,18 +947,70 @@ int fp4_ctas(const AttendFp4Params &p, int ne, bool listed) {
   if (listed && p.B <= budget) return p.B * std::max(1, std::min(budget / p.B, tiles / least));
   return (int)std::max<long long>(1, std::min<long long>(budget, std::max<long long>(std::min(p.B, budget), (long long)p.B * tiles / least)));
 }
+template <int C>
+int fp4_attr() {
+  static std::atomic<bool> attr_dev[kMaxDevices];
+  std::atomic<bool> &attr = attr_dev[device_slot()];
+  if (!attr) {
+    const cudaError_t e = cudaFuncSetAttribute(attend_fp4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)Fp4Layout<C>::bytes);
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();
+      return fail(HCA_ERR_CUDA, "attend_fp4 smem attribute: %s", cudaGetErrorString(e));
+    }
+    attr = true;
+  }
+  return HCA_OK;
+}
+template <int C>
+cudaLaunchConfig_t fp4_config(int G, int S, cudaLaunchAttribute *at) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(G, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Fp4Layout<C>::bytes;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = S;
+  at->val.clusterDim.y = at->val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = S ? 1 : 0;
+  return cfg;
+}
+// Clusters of S CTAs, one to an SM, that the GPU holds at once: fewer than its
+// SMs over S, since a cluster stays within a group of SMs (of 8: 15, not 18).
+template <int C>
+int fp4_resident(int S) {
+  static std::atomic<int> n_dev[kMaxDevices][9];
+  std::atomic<int> &n = n_dev[device_slot()][S];
+  if (!n) {
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = fp4_config<C>(S, S, &at);
+    int v = 0;
+    if (fp4_attr<C>() || cudaOccupancyMaxActiveClusters(&v, attend_fp4_kernel<C>, &cfg) != cudaSuccess || v <= 0) {
+      (void)cudaGetLastError();
+      v = std::max(1, num_sms() / S);   // the launch reports what is wrong
+    }
+    n = v;
+  }
+  return n;
+}
+int fp4_resident(const AttendFp4Params &p, int S) {
+  return p.c == 128 ? fp4_resident<128>(S) : p.c == 256 ? fp4_resident<256>(S) : fp4_resident<512>(S);
+}
 // CTAs per sequence where a cluster takes each sequence and joins it through
 // shared memory: no parts in the workspace and no second launch, which cost as
 // much as about 4 tiles, but at most 8 CTAs, and a ragged batch waits for its
 // longest sequence (half of the most tiles is taken as the mean where only the
 // positions tell).  0 where runs over all sequences have that much less.  32
 // sequences of 10 tiles at 64 x 512: 19.3 us in clusters of 4, 24.3 as runs;
-// one of 10 tiles at 16 x 128: 9.3 us in a cluster of 8, 10.0 as runs.
+// one of 10 tiles at 16 x 128: 9.3 us in a cluster of 8, 10.0 as runs.  Clusters
+// that the GPU does not hold at once wait for others to end: 16 sequences of 10
+// tiles at 64 x 512 took 31.7 us in clusters of 8, 18.5 in clusters of 4; 36 of
+// them 36.0 in clusters of 4, 24.8 in clusters of 2.
 int fp4_cluster(const AttendFp4Params &p, int ne, bool listed) {
   const int sms = num_sms(), budget = p.max_ctas > 0 && p.max_ctas < sms ? p.max_ctas : sms;
   const int nw = std::min(p.w, p.max_pos + 1), tiles = (nw + KT - 1) / KT + (ne + KT - 1) / KT;
   int S = 1;
-  while (S < 8 && 2 * S <= tiles && (long long)p.B * 2 * S <= budget) S *= 2;
+  while (S < 8 && 2 * S <= tiles && (long long)p.B * 2 * S <= budget && p.B <= fp4_resident(p, 2 * S)) S *= 2;
   if (S == 1) return 0;
   const int runs = (int)(((long long)p.B * tiles + fp4_ctas(p, ne, listed) - 1) / fp4_ctas(p, ne, listed));
   return (tiles + S - 1) / S <= (listed ? runs : runs / 2) + 4 ? S : 0;
@@ -968,26 +1020,11 @@ size_t fp4_part_bytes(const AttendFp4Params &p, size_t G) { return fp4_align(2 *
 
 template <int C>
 int launch_fp4(const AttendFp4Params &p, const Fp4Plan &pl, cudaStream_t s) {
-  static std::atomic<bool> attr_dev[kMaxDevices];
-  std::atomic<bool> &attr = attr_dev[device_slot()];
-  if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(attend_fp4_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)Fp4Layout<C>::bytes);
-    if (e != cudaSuccess) return fail(HCA_ERR_CUDA, "attend_fp4 smem attribute: %s", cudaGetErrorString(e));
-    attr = true;
-  }
+  if (const int rc = fp4_attr<C>()) return rc;
   LaunchScope ls("attend_fp4", s);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(pl.G, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Fp4Layout<C>::bytes;
+  cudaLaunchAttribute at;
+  cudaLaunchConfig_t cfg = fp4_config<C>(pl.G, pl.S, &at);
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = pl.S;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = pl.S ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_fp4_kernel<C>, p, pl);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
