@@ -1002,7 +1002,9 @@ int fp4_resident(const AttendFp4Params &p, int S) {
 // longest sequence (half of the most tiles is taken as the mean where only the
 // positions tell).  0 where runs over all sequences have that much less.  32
 // sequences of 10 tiles at 64 x 512: 19.3 us in clusters of 4, 24.3 as runs;
-// one of 10 tiles at 16 x 128: 9.3 us in a cluster of 8, 10.0 as runs.  Clusters
+// one of 10 tiles at 16 x 128: 9.3 us in a cluster of 8, 10.0 as runs; 64 x 512
+// with positions spread over 0.4 to 1 of the most entries: 30 sequences of 1000
+// 21.9 us in clusters, 27.3 as runs, 8 of 7500 38.4 and 31.0.  Clusters
 // that the GPU does not hold at once wait for others to end: 16 sequences of 10
 // tiles at 64 x 512 took 31.7 us in clusters of 8, 18.5 in clusters of 4; 36 of
 // them 36.0 in clusters of 4, 24.8 in clusters of 2.
@@ -1068,6 +1070,8 @@ int run_attend_fp4(const AttendFp4Params &p, void *ws, size_t, cudaStream_t s) {
   LaunchScope ls("attend_fp4_combine", s);
   cudaLaunchConfig_t cfg{};
   // a part-parallel block per column group where that is at most a wave of blocks
+  // (ragged, 12000 entries: 8 sequences at 16 x 128 20.2 us, 27.1 with a warp per
+  // group; 20 at 64 x 512 57.7, with a warp 54.2)
   const bool few = (long long)p.B * (p.c / 8) * ((p.n_h + 15) / 16) <= 16LL * num_sms();
   cfg.gridDim = dim3(p.B, few ? p.c / 8 : p.c / 32, (p.n_h + 15) / 16);
   cfg.blockDim = dim3(128, 1, 1);

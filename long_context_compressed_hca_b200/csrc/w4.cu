@@ -182,7 +182,10 @@ W4Work w4_work(const W4Params &p, int tn) {
   w.G = std::min(num_sms(), w.U);
   w.gran = 1;
   // whole tiles per CTA where the longest run gets at most 6 units longer by
-  // it: joining parts costs a launch, 2 to 3 us, and a unit about 0.4
+  // it: joining parts costs a launch, 2 to 3 us, and a unit about 0.4.  5 longer:
+  // 64 tokens x 12800 x 4096 13.2 us, cut 15.7; 6 longer: 64 x 9600 x 3328 11.8,
+  // cut 13.5; 7 longer: 16 x 19200 x 2048 13.1, cut 12.2; 9 longer: 16 x 20480 x
+  // 2560 12.8, cut 11.7
   const int wt = (tiles + num_sms() - 1) / num_sms();
   if (wt * w.nk <= (w.U + w.G - 1) / w.G + 6) {
     w.gran = w.nk;
