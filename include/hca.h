@@ -496,9 +496,10 @@ int hca_add_rms_norm(const hca_norm_desc *d, const void *x, const void *res, con
  *   with ldn = N rounded up to 16; row_scale [groups*N] fp32.
  * x [T, groups*K] HCA_BF16 (x_scale NULL) or HCA_FP8E4M3 (x_scale [T] fp32);
  *   out [T, groups*N] HCA_F32 or HCA_BF16; row strides ldx, ldo elements
- *   (0 = dense).  Sums are fp32 and run in a fixed order.  A bf16 x enters them
- *   exactly down to 2^-31 of the largest |x| of its token and group, and to
- *   2^-39 of that largest below.
+ *   (0 = dense).  Sums are fp32 and run in a fixed order; the tensor cores add
+ *   16 products at a time and cut the sum off instead of rounding it (2^-23 of
+ *   the magnitudes' sum each time).  A bf16 x enters exactly down to 2^-31 of
+ *   the largest |x| of its token and group, and to 2^-39 of that largest below.
  * K a multiple of 32 and of scale_group (32, 64 or 128), K <= 32768; N >= 1,
  *   T >= 0 (T = 0 is a no-op), groups >= 1.  Rows of x must start at multiples
  *   of 16 bytes.  Meant for decode batches: beyond 64 tokens the weights are
@@ -575,6 +576,9 @@ typedef struct {
  * hca_kv_fp4_row_bytes; sink [n_h] fp32, NULL = no sink (+infinity: zeros,
  * -infinity: no sink for that head); kv_mixed must be 0;
  * max_ctas as in hca_attend; B times the most keys of a sequence below 2^37.
+ * Sums, maxima and the denominator are fp32; each probability is rounded to
+ * bf16 (2^-8 of itself at most) where it multiplies its row, and the rotation's
+ * sine and cosine are within 2^-20.
  * q and KV values must be finite.  o may not overlap an input or ws.
  * ws: scratch of hca_attend_fp4_workspace_size bytes (16-byte aligned), which
  * calls that may overlap in time must not share. */

@@ -31,7 +31,7 @@
 //                    grows by more than 2^8, P in bf16 (its rounding, 2^-8 of
 //                    p, is that of the bf16 output; sums and statistics fp32)
 // Bound: a tile takes 3250 cycles of a CTA at c = 512 (32 sequences of 16384
-// entries: 120 us).  M = 64 uses half the tensor pipe, 2460 cycles of MMAs; the
+// entries: 122 us).  M = 64 uses half the tensor pipe, 2460 cycles of MMAs; the
 // loader warps need 3100, about the same with the conversion by other
 // instructions (byte lookups in the integer pipe, a mixture of both) or ordered
 // otherwise, and wait for 300.  64 x 368 bytes of HBM are 1000 cycles of an
@@ -1001,8 +1001,8 @@ int fp4_resident(const AttendFp4Params &p, int S) {
 // much as about 4 tiles, but at most 8 CTAs, and a ragged batch waits for its
 // longest sequence (half of the most tiles is taken as the mean where only the
 // positions tell).  0 where runs over all sequences have that much less.  32
-// sequences of 10 tiles at 64 x 512: 19.3 us in clusters of 4, 24.3 as runs;
-// one of 10 tiles at 16 x 128: 9.3 us in a cluster of 8, 10.0 as runs; 64 x 512
+// sequences of 10 tiles at 64 x 512: 19.6 us in clusters of 4, 23.9 as runs;
+// one of 10 tiles at 16 x 128: 9.5 us in a cluster of 8, 9.9 as runs; 64 x 512
 // with positions spread over 0.4 to 1 of the most entries: 30 sequences of 1000
 // 21.9 us in clusters, 27.3 as runs, 8 of 7500 38.4 and 31.0.  Clusters
 // that the GPU does not hold at once wait for others to end: 16 sequences of 10

@@ -111,3 +111,12 @@ def test_two_streams_at_once(cuda):
     torch.cuda.synchronize()
     for i in range(2):
         assert torch.equal(outs[i], alone[i]) and torch.equal(ys[2 + i], ys[i])
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second GPU")
+def test_tensors_of_another_device_are_refused(cuda):
+    other = torch.device("cuda:1")
+    x, out = torch.zeros(4, 512, dtype=BF16, device=other), torch.zeros(4, 512, dtype=BF16, device=other)
+    _refused("current CUDA device", lambda: hb.add_rms_norm(hb.norm_desc(4, 512), x, None, None, None, out))
+    _refused("current CUDA device", lambda: hb.w4_quantize(hb.w4_desc(0, 4, 512), x))
+    _refused("current CUDA device", lambda: hb.kv_quant_fp4(x, 512, 64, torch.zeros(4, 368, dtype=U8, device=cuda)))
